@@ -1,7 +1,8 @@
 /*
- * lsh_attn.h -- C ABI of liblsh_attn.so, the B200 (sm_100a) LSH attention
- * forward pass: shared-QK attention restricted by random-rotation hashing,
- * as described in "Reformer: The Efficient Transformer" (arXiv 2001.04451v2):
+ * lsh_attn.h -- C ABI of liblsh_attn.so, LSH attention for the B200 (sm_100a)
+ * and, further down, the operators of a language model around it (token table
+ * and cross entropy, tokens sorted by expert).  The attention is shared-QK
+ * attention restricted by random-rotation hashing, as described in "Reformer: The Efficient Transformer" (arXiv 2001.04451v2):
  *   section 2 "LSH attention"     -- hash h(x) = argmax([xR; -xR]), sort by
  *                                    bucket, attend within sorted chunks;
  *   section 2 "Causal masking"    -- positions follow the same permutation,
@@ -24,8 +25,9 @@
  *    *_workspace_size queries).  The two places where it holds device
  *    resources of its own are stated at their calls: lsh_attn_forward_host's
  *    streams and events, and lsh_attn_forward_noalloc's built-in scratch.
- *  - Every device pointer must be 16-byte aligned.  Tensors are dense,
- *    row-major, last dimension fastest.
+ *  - Every device pointer must be 16-byte aligned; of the token table's and
+ *    the routing calls' vectors (one value per token or entry) only aligned
+ *    to their values.  Tensors are dense, row-major, last dimension fastest.
  *  - `stream` is a cudaStream_t passed as void* (NULL = the legacy default
  *    stream).  All work is enqueued on it; no call synchronises the host
  *    except lsh_attn_device_check().
@@ -311,6 +313,156 @@ LSH_ATTN_API lsh_status lsh_attn_forward_host(const lsh_shape* shape, const void
 LSH_ATTN_API lsh_status lsh_attn_forward_noalloc(const lsh_shape* shape, const void* qk,
                                                  const void* v, const void* rotations,
                                                  void* out, float* lse, void* stream);
+
+/* ---------------------------------------------------------------------- *
+ * The token table of a language model on this attention: its lookup, the
+ * lookup's gradient, and the loss against it.  (The paper computes the loss
+ * of a large vocabulary in sections; the table's two ends are this library's
+ * addition.)
+ *   rows      n  tokens, of any number of sequences; 0 is allowed.
+ *   vocab     V  rows of the table, 1 <= V <= 2^20.
+ *   d_model   D  a multiple of 8 in [8, 16384].
+ *   dtype     lsh_dtype of the table and of every row of D values.
+ *   index_type  lsh_index_type of tokens and targets.
+ *   scale     finite; see each call.
+ *   flags     0 or LSH_FLAG_PORTABLE (cross entropy: CUDA cores only).
+ * A token or target outside [0, V) is no error: padding (-1, say) gives a row
+ * of zeros, no loss and no gradient.
+ * ---------------------------------------------------------------------- */
+typedef enum lsh_index_type {
+  LSH_I32 = 0,                 /* int32 */
+  LSH_I64 = 1                  /* int64 */
+} lsh_index_type;
+
+typedef struct lsh_table {
+  int64_t rows;        /* n: 0 <= n <= 2^30                                  */
+  int32_t vocab;
+  int32_t d_model;
+  int32_t dtype;
+  int32_t index_type;
+  float scale;
+  uint32_t flags;
+} lsh_table;
+
+/* Lookup: out[t] = scale * table[tokens[t]], a zero row for padding.
+ *   tokens [n] index type; table [V, D] dtype; out [n, D] dtype out.       */
+LSH_ATTN_API lsh_status lsh_attn_embed(const lsh_table* shape, const void* tokens,
+                                       const void* table, void* out, void* stream);
+
+/* Its gradient: dtable[v] = init[v] + scale * sum over tokens[t] == v of
+ * dout[t], the sum in float32 and rounded once.  The tokens are sorted on the
+ * device and every row of dtable is written once, without atomics: the same
+ * input gives the same bits.
+ *   dout [n, D] dtype; init [V, D] dtype, NULL for zeros, and may be dtable
+ *   itself (the gradient is added in place); dtable [V, D] dtype out.
+ *   workspace: at least lsh_attn_embed_backward_workspace_size() bytes,
+ *   256-byte aligned (may be NULL when that is 0).                          */
+LSH_ATTN_API lsh_status lsh_attn_embed_backward_workspace_size(const lsh_table* shape,
+                                                               size_t* bytes);
+LSH_ATTN_API lsh_status lsh_attn_embed_backward(const lsh_table* shape, const void* tokens,
+                                                const void* dout, const void* init,
+                                                void* dtable, void* workspace,
+                                                size_t workspace_bytes, void* stream);
+
+/* Softmax cross entropy of every row against the whole table, the logits
+ * never stored:
+ *   z_iv = scale x_i . table_v,  lse_i = log sum_v exp(z_iv),
+ *   loss_i = lse_i - z_i,targets_i, and 0 for padding (lse is still given).
+ *   x [n, D] dtype; table [V, D] dtype; targets [n] index type; loss, lse
+ *   [n] float32 out.
+ *   workspace: at least lsh_attn_xent_workspace_size() bytes, 256-byte
+ *   aligned (may be NULL when that is 0).                                   */
+LSH_ATTN_API lsh_status lsh_attn_xent_workspace_size(const lsh_table* shape, size_t* bytes);
+LSH_ATTN_API lsh_status lsh_attn_xent(const lsh_table* shape, const void* x, const void* table,
+                                      const void* targets, float* loss, float* lse,
+                                      void* workspace, size_t workspace_bytes, void* stream);
+
+/* Its gradients for the upstream gradient dloss [n] float32 of loss:
+ *   g_iv = scale dloss_i (exp(z_iv - lse_i) - [v == targets_i]),
+ *   dx_i = sum_v g_iv table_v,  dtable_v = sum_i g_iv x_i,
+ * lse as the forward gave it.  Rows of padding get dx = 0 and take no part in
+ * dtable, whatever x and dloss hold there.
+ *   dx [n, D] dtype out; dtable [V, D] dtype out.  With bfloat16, g is rounded
+ *   to bfloat16 before the two products; they are summed in float32.
+ *   workspace: at least lsh_attn_xent_backward_workspace_size() bytes,
+ *   256-byte aligned (may be NULL when that is 0).                          */
+LSH_ATTN_API lsh_status lsh_attn_xent_backward_workspace_size(const lsh_table* shape,
+                                                              size_t* bytes);
+LSH_ATTN_API lsh_status lsh_attn_xent_backward(const lsh_table* shape, const void* x,
+                                               const void* table, const void* targets,
+                                               const float* lse, const float* dloss, void* dx,
+                                               void* dtable, void* workspace,
+                                               size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------- *
+ * Tokens sorted by expert and back, for a feed-forward layer whose rows are
+ * routed (the routing-style assignment's counterpart outside attention).
+ * Entry (t, j) is token t's j-th expert; entries are numbered t * k + j.
+ *   tokens    T  0 is allowed; T * k <= 2^30.
+ *   top_k     k  1..64 experts per token.
+ *   n_experts E  1..1023.
+ *   d_model   D  a multiple of 8 in [8, 16384].
+ *   dtype     lsh_dtype of the rows; weights and their gradients are float32.
+ *   index_type  lsh_index_type of the router's choice.
+ * ---------------------------------------------------------------------- */
+typedef struct lsh_route {
+  int64_t tokens;
+  int32_t top_k;
+  int32_t n_experts;
+  int32_t d_model;
+  int32_t dtype;
+  int32_t index_type;
+  uint32_t flags;      /* 0                                                  */
+} lsh_route;
+
+/* The plan: entries in stable order by expert; an expert outside [0, E)
+ * drops its entry (over capacity, padding), and dropped entries come last.
+ * A token may name the same expert twice.
+ *   experts [T, k] index type.
+ *   perm    [T * k] int32 out: the entry in slot s.
+ *   undo    [T, k]  int32 out: the slot of entry (t, j).
+ *   offsets [E + 1] int32 out: expert e has slots offsets[e] .. offsets[e+1]-1;
+ *           slots from offsets[E] on hold dropped entries.
+ *   workspace: at least lsh_attn_route_sort_workspace_size() bytes, 256-byte
+ *   aligned (may be NULL when that is 0).  d_model and dtype are not used.  */
+LSH_ATTN_API lsh_status lsh_attn_route_sort_workspace_size(const lsh_route* shape,
+                                                           size_t* bytes);
+LSH_ATTN_API lsh_status lsh_attn_route_sort(const lsh_route* shape, const void* experts,
+                                            int32_t* perm, int32_t* undo, int32_t* offsets,
+                                            void* workspace, size_t workspace_bytes,
+                                            void* stream);
+
+/* xs[undo[t, j]] = x[t]; zero rows in the slots of dropped entries.
+ *   x [T, D]; xs [T * k, D] out.                                            */
+LSH_ATTN_API lsh_status lsh_attn_route_gather(const lsh_route* shape, const void* x,
+                                              const int32_t* undo, const int32_t* offsets,
+                                              void* xs, void* stream);
+
+/* The gather's gradient: dx[t] = sum over kept j of dxs[undo[t, j]], summed in
+ * float32 in the order of j.  Rows of dropped entries are not read.
+ *   dxs [T * k, D]; dx [T, D] out.                                          */
+LSH_ATTN_API lsh_status lsh_attn_route_gather_backward(const lsh_route* shape, const void* dxs,
+                                                       const int32_t* undo,
+                                                       const int32_t* offsets, void* dx,
+                                                       void* stream);
+
+/* out[t] = sum over kept j of weights[t, j] * y[undo[t, j]], summed in float32
+ * in the order of j; a zero row for a token with no kept entry.  Rows and
+ * weights of dropped entries are not read.
+ *   y [T * k, D]; weights [T, k] float32; out [T, D] out.                   */
+LSH_ATTN_API lsh_status lsh_attn_route_combine(const lsh_route* shape, const void* y,
+                                               const float* weights, const int32_t* undo,
+                                               const int32_t* offsets, void* out, void* stream);
+
+/* The combine's gradients for dout [T, D]: dy[undo[t, j]] = weights[t, j] *
+ * dout[t] and dweights[t, j] = dout[t] . y[undo[t, j]]; zero for dropped
+ * entries.
+ *   dy [T * k, D] out; dweights [T, k] float32 out.                         */
+LSH_ATTN_API lsh_status lsh_attn_route_combine_backward(const lsh_route* shape, const void* dout,
+                                                        const void* y, const float* weights,
+                                                        const int32_t* undo,
+                                                        const int32_t* offsets, void* dy,
+                                                        float* dweights, void* stream);
 
 /* ---------------------------------------------------------------------- *
  * Diagnostics.

@@ -1,4 +1,5 @@
-"""B200 (sm_100a) LSH attention forward pass: Python binding of liblsh_attn.so.
+"""B200 (sm_100a) LSH attention and the operators of a language model around it
+(token table, cross entropy, expert routing): Python binding of liblsh_attn.so.
 
 The functions here carry the names of the C ABI in ``include/lsh_attn.h`` and
 only marshal arguments: they check dtype/device/contiguity, allocate output
@@ -12,6 +13,7 @@ Build the library first:  python -m lsh_bucketed_sparse_b200.build
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -26,8 +28,15 @@ __all__ = [
     "lsh_attn_forward_workspace_size", "lsh_attn_forward_host",
     "lsh_attn_forward_host_device_bytes", "lsh_attn_device_check", "lsh_attn_forward_noalloc",
     "lsh_attn_backward", "lsh_attn_backward_workspace_size", "lsh_attn_kernel_launches",
+    "TableShape", "RouteShape", "make_table_shape", "make_route_shape",
+    "lsh_attn_embed", "lsh_attn_embed_backward", "lsh_attn_embed_backward_workspace_size",
+    "lsh_attn_xent", "lsh_attn_xent_workspace_size",
+    "lsh_attn_xent_backward", "lsh_attn_xent_backward_workspace_size",
+    "lsh_attn_route_sort", "lsh_attn_route_sort_workspace_size",
+    "lsh_attn_route_gather", "lsh_attn_route_gather_backward",
+    "lsh_attn_route_combine", "lsh_attn_route_combine_backward",
     "LIB_PATH", "HEADER_PATH", "NOALLOC_SCRATCH_BYTES",
-    "F32", "BF16", "FLAG_PORTABLE", "FLAG_DEDUP", "FLAG_BUCKET_MASK", "FLAG_KMEANS",
+    "F32", "BF16", "I32", "I64", "FLAG_PORTABLE", "FLAG_DEDUP", "FLAG_BUCKET_MASK", "FLAG_KMEANS",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -35,6 +44,7 @@ LIB_PATH = os.path.join(_PKG, "_lib", "liblsh_attn.so")
 HEADER_PATH = os.path.join(os.path.dirname(_PKG), "include", "lsh_attn.h")
 
 F32, BF16 = 0, 1
+I32, I64 = 0, 1
 FLAG_PORTABLE = 1
 FLAG_DEDUP = 2
 FLAG_BUCKET_MASK = 4
@@ -58,10 +68,28 @@ class Shape(ctypes.Structure):
                 ("dtype", ctypes.c_int32), ("flags", ctypes.c_uint32)]
 
 
+class TableShape(ctypes.Structure):
+    """lsh_table: rows of tokens against a token table."""
+    _fields_ = [("rows", ctypes.c_int64), ("vocab", ctypes.c_int32),
+                ("d_model", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("index_type", ctypes.c_int32), ("scale", ctypes.c_float),
+                ("flags", ctypes.c_uint32)]
+
+
+class RouteShape(ctypes.Structure):
+    """lsh_route: tokens and the experts they go to."""
+    _fields_ = [("tokens", ctypes.c_int64), ("top_k", ctypes.c_int32),
+                ("n_experts", ctypes.c_int32), ("d_model", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("index_type", ctypes.c_int32),
+                ("flags", ctypes.c_uint32)]
+
+
 _lib = None
 _P = ctypes.c_void_p
 _SZ = ctypes.c_size_t
 _SHP = ctypes.POINTER(Shape)
+_TAB = ctypes.POINTER(TableShape)
+_RTE = ctypes.POINTER(RouteShape)
 _SIGS = {
     "lsh_attn_hash": [_SHP, _P, _P, _P, _P, _P],
     "lsh_attn_sort_workspace_size": [_SHP, ctypes.POINTER(_SZ)],
@@ -76,6 +104,19 @@ _SIGS = {
     "lsh_attn_forward_noalloc": [_SHP, _P, _P, _P, _P, _P, _P],
     "lsh_attn_backward_workspace_size": [_SHP, ctypes.POINTER(_SZ)],
     "lsh_attn_backward": [_SHP, _P, _P, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P],
+    "lsh_attn_embed": [_TAB, _P, _P, _P, _P],
+    "lsh_attn_embed_backward_workspace_size": [_TAB, ctypes.POINTER(_SZ)],
+    "lsh_attn_embed_backward": [_TAB, _P, _P, _P, _P, _P, _SZ, _P],
+    "lsh_attn_xent_workspace_size": [_TAB, ctypes.POINTER(_SZ)],
+    "lsh_attn_xent": [_TAB, _P, _P, _P, _P, _P, _P, _SZ, _P],
+    "lsh_attn_xent_backward_workspace_size": [_TAB, ctypes.POINTER(_SZ)],
+    "lsh_attn_xent_backward": [_TAB, _P, _P, _P, _P, _P, _P, _P, _P, _SZ, _P],
+    "lsh_attn_route_sort_workspace_size": [_RTE, ctypes.POINTER(_SZ)],
+    "lsh_attn_route_sort": [_RTE, _P, _P, _P, _P, _P, _SZ, _P],
+    "lsh_attn_route_gather": [_RTE, _P, _P, _P, _P, _P],
+    "lsh_attn_route_gather_backward": [_RTE, _P, _P, _P, _P, _P],
+    "lsh_attn_route_combine": [_RTE, _P, _P, _P, _P, _P, _P],
+    "lsh_attn_route_combine_backward": [_RTE, _P, _P, _P, _P, _P, _P, _P, _P],
     "lsh_attn_status_string": [ctypes.c_int],
     "lsh_attn_last_error": [],
     "lsh_attn_device_check": [_P],
@@ -433,3 +474,256 @@ def lsh_attn_backward(qk, v, inv_norm, perm, out, lse, dout, chunk_len, causal, 
                                    _ptr(dv), _ptr(workspace), _SZ(workspace.numel()),
                                    _stream(stream)))
     return dqk, dv
+
+
+# ---- token table, cross entropy, expert routing ------------------------------
+def _index_code(t: torch.Tensor, name: str) -> int:
+    if t.dtype == torch.int32:
+        return I32
+    if t.dtype == torch.int64:
+        return I64
+    raise TypeError(f"{name} must be int32 or int64, got {t.dtype}")
+
+
+def make_table_shape(rows, vocab, d_model, dtype=torch.bfloat16, index_type=I64, scale=1.0,
+                     portable=False) -> TableShape:
+    return TableShape(rows, vocab, d_model, dtype if isinstance(dtype, int) else _dtype_code(dtype),
+                      index_type, scale, FLAG_PORTABLE if portable else 0)
+
+
+def make_route_shape(tokens, top_k, n_experts, d_model=8, dtype=torch.bfloat16,
+                     index_type=I64) -> RouteShape:
+    return RouteShape(tokens, top_k, n_experts, d_model,
+                      dtype if isinstance(dtype, int) else _dtype_code(dtype), index_type, 0)
+
+
+@contextlib.contextmanager
+def _launching(device, stream):
+    """Makes ``device`` and ``stream`` current (the device's own current stream
+    when None), so that what is allocated inside belongs to the stream the
+    kernels run on, and yields the stream's handle."""
+    with torch.cuda.device(device):
+        if stream is None:
+            yield ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+            return
+        if stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, expected {device}")
+        with torch.cuda.stream(stream):
+            yield ctypes.c_void_p(stream.cuda_stream)
+
+
+def _size(query, shape) -> int:
+    n = _SZ()
+    _check(query(ctypes.byref(shape), ctypes.byref(n)))
+    return n.value
+
+
+def _workspace(workspace, need, like):
+    """The caller's uint8 workspace, or a new one; None when none is needed."""
+    if workspace is not None:
+        _cuda(workspace, "workspace", torch.uint8, None, like)
+        return workspace, workspace.numel()
+    if need == 0:
+        return None, 0
+    return torch.empty(need, dtype=torch.uint8, device=like.device), need
+
+
+def _out(t, name, dtype, shape, like):
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    return _cuda(t, name, dtype, shape, like)
+
+
+def _table(table, d=None, like=None):
+    _cuda(table, "table", None, None, like)
+    if table.dim() != 2 or (d is not None and table.shape[1] != d):
+        raise ValueError(f"table must be [vocab, {'d_model' if d is None else d}], got shape "
+                         f"{tuple(table.shape)}")
+    return table.shape
+
+
+def lsh_attn_embed(tokens, table, *, scale=1.0, out=None, stream=None):
+    """Lookup: scale * table[tokens], zero rows for tokens outside the table.
+    tokens int32 or int64 of any shape [...]; table [V, D].  Returns
+    [..., D] in the table's dtype."""
+    _cuda(tokens, "tokens")
+    V, D = _table(table, None, tokens)
+    shp = make_table_shape(tokens.numel(), V, D, table.dtype, _index_code(tokens, "tokens"), scale)
+    with _launching(tokens.device, stream) as st:
+        out = _out(out, "out", table.dtype, (*tokens.shape, D), tokens)
+        _check(lib().lsh_attn_embed(ctypes.byref(shp), _ptr(tokens), _ptr(table), _ptr(out), st))
+    return out
+
+
+def lsh_attn_embed_backward_workspace_size(shape: TableShape) -> int:
+    return _size(lib().lsh_attn_embed_backward_workspace_size, shape)
+
+
+def lsh_attn_embed_backward(tokens, dout, vocab, *, scale=1.0, init=None, out=None,
+                            workspace=None, stream=None):
+    """The lookup's gradient for dout [..., D]: [vocab, D] in dout's dtype,
+    init + scale * (the sum of dout over each token), summed in float32.
+    ``init`` (a gradient that is there already) and ``out`` may be the same
+    tensor.  The same inputs give the same bits."""
+    _cuda(tokens, "tokens")
+    _cuda(dout, "dout", None, None, tokens)
+    if dout.dim() < 1 or dout.shape[:-1] != tokens.shape:
+        raise ValueError(f"dout must be {[*tokens.shape]} + [d_model], got shape "
+                         f"{tuple(dout.shape)}")
+    D = dout.shape[-1]
+    if init is not None:
+        _cuda(init, "init", dout.dtype, (vocab, D), tokens)
+    shp = make_table_shape(tokens.numel(), vocab, D, dout.dtype, _index_code(tokens, "tokens"),
+                           scale)
+    need = lsh_attn_embed_backward_workspace_size(shp)
+    with _launching(tokens.device, stream) as st:
+        out = _out(out, "out", dout.dtype, (vocab, D), tokens)
+        ws, n = _workspace(workspace, need, tokens)
+        _check(lib().lsh_attn_embed_backward(ctypes.byref(shp), _ptr(tokens), _ptr(dout),
+                                             _ptr(init), _ptr(out), _ptr(ws), _SZ(n), st))
+    return out
+
+
+def _xent_args(x, table, targets, scale, portable):
+    _cuda(x, "x")
+    if x.dim() < 1:
+        raise ValueError("x must be [..., d_model]")
+    D = x.shape[-1]
+    _cuda(targets, "targets", None, x.shape[:-1], x)
+    V, _ = _table(table, D, x)
+    if table.dtype != x.dtype:
+        raise TypeError(f"table must be {x.dtype}, got {table.dtype}")
+    return make_table_shape(targets.numel(), V, D, x.dtype, _index_code(targets, "targets"),
+                            scale, portable)
+
+
+def lsh_attn_xent_workspace_size(shape: TableShape) -> int:
+    return _size(lib().lsh_attn_xent_workspace_size, shape)
+
+
+def lsh_attn_xent(x, table, targets, *, scale=1.0, workspace=None, portable=False, stream=None):
+    """Softmax cross entropy of every row of x [..., D] against the whole table
+    [V, D], the logits scale * x @ table.T never stored.  Returns (loss, lse),
+    float32 [...]; loss is 0 where the target is outside the table."""
+    shp = _xent_args(x, table, targets, scale, portable)
+    need = lsh_attn_xent_workspace_size(shp)
+    with _launching(x.device, stream) as st:
+        loss = _out(None, "loss", torch.float32, targets.shape, x)
+        lse = _out(None, "lse", torch.float32, targets.shape, x)
+        ws, n = _workspace(workspace, need, x)
+        _check(lib().lsh_attn_xent(ctypes.byref(shp), _ptr(x), _ptr(table), _ptr(targets),
+                                   _ptr(loss), _ptr(lse), _ptr(ws), _SZ(n), st))
+    return loss, lse
+
+
+def lsh_attn_xent_backward_workspace_size(shape: TableShape) -> int:
+    return _size(lib().lsh_attn_xent_backward_workspace_size, shape)
+
+
+def lsh_attn_xent_backward(x, table, targets, lse, dloss, *, scale=1.0, workspace=None,
+                           portable=False, stream=None):
+    """Gradients of lsh_attn_xent's loss for the upstream dloss, float32 [...],
+    with the forward's lse.  Returns (dx [..., D], dtable [V, D]) in x's dtype."""
+    shp = _xent_args(x, table, targets, scale, portable)
+    _cuda(lse, "lse", torch.float32, targets.shape, x)
+    _cuda(dloss, "dloss", torch.float32, targets.shape, x)
+    need = lsh_attn_xent_backward_workspace_size(shp)
+    with _launching(x.device, stream) as st:
+        dx = _out(None, "dx", x.dtype, x.shape, x)
+        dtable = _out(None, "dtable", x.dtype, table.shape, x)
+        ws, n = _workspace(workspace, need, x)
+        _check(lib().lsh_attn_xent_backward(ctypes.byref(shp), _ptr(x), _ptr(table),
+                                            _ptr(targets), _ptr(lse), _ptr(dloss), _ptr(dx),
+                                            _ptr(dtable), _ptr(ws), _SZ(n), st))
+    return dx, dtable
+
+
+def lsh_attn_route_sort_workspace_size(shape: RouteShape) -> int:
+    return _size(lib().lsh_attn_route_sort_workspace_size, shape)
+
+
+def lsh_attn_route_sort(experts, n_experts, *, workspace=None, stream=None):
+    """The plan of a routed layer: experts [T, k] (int32 or int64; an id outside
+    [0, n_experts) drops its entry) in stable order by expert, dropped entries
+    last.  Returns int32 (perm [T * k], the entry t * k + j in each slot;
+    undo [T, k], the slot of each entry; offsets [n_experts + 1], each
+    expert's first slot, offsets[-1] the first dropped one)."""
+    _cuda(experts, "experts")
+    if experts.dim() != 2:
+        raise ValueError(f"experts must be [tokens, top_k], got shape {tuple(experts.shape)}")
+    T, k = experts.shape
+    shp = make_route_shape(T, k, n_experts, index_type=_index_code(experts, "experts"))
+    need = lsh_attn_route_sort_workspace_size(shp)
+    with _launching(experts.device, stream) as st:
+        perm = torch.empty(T * k, dtype=torch.int32, device=experts.device)
+        undo = torch.empty(T, k, dtype=torch.int32, device=experts.device)
+        offsets = torch.empty(n_experts + 1, dtype=torch.int32, device=experts.device)
+        ws, n = _workspace(workspace, need, experts)
+        _check(lib().lsh_attn_route_sort(ctypes.byref(shp), _ptr(experts), _ptr(perm), _ptr(undo),
+                                         _ptr(offsets), _ptr(ws), _SZ(n), st))
+    return perm, undo, offsets
+
+
+def _route_args(rows, name, per_entry, undo, offsets):
+    """rows [T, D], or [T * k, D] when per_entry, with the plan of route_sort."""
+    _cuda(rows, name)
+    _cuda(undo, "undo", torch.int32, None, rows)
+    _cuda(offsets, "offsets", torch.int32, None, rows)
+    if undo.dim() != 2:
+        raise ValueError(f"undo must be [tokens, top_k], got shape {tuple(undo.shape)}")
+    if offsets.dim() != 1 or offsets.numel() < 2:
+        raise ValueError(f"offsets must be [n_experts + 1], got shape {tuple(offsets.shape)}")
+    T, k = undo.shape
+    n = T * k if per_entry else T
+    if rows.dim() != 2 or rows.shape[0] != n:
+        raise ValueError(f"{name} must be [{n}, d_model], got shape {tuple(rows.shape)}")
+    return make_route_shape(T, k, offsets.numel() - 1, rows.shape[1], rows.dtype)
+
+
+def lsh_attn_route_gather(x, undo, offsets, *, out=None, stream=None):
+    """Tokens in their experts' order: x [T, D] to [T * k, D], zero rows in the
+    slots of dropped entries."""
+    shp = _route_args(x, "x", False, undo, offsets)
+    with _launching(x.device, stream) as st:
+        out = _out(out, "out", x.dtype, (undo.numel(), x.shape[1]), x)
+        _check(lib().lsh_attn_route_gather(ctypes.byref(shp), _ptr(x), _ptr(undo), _ptr(offsets),
+                                           _ptr(out), st))
+    return out
+
+
+def lsh_attn_route_gather_backward(dxs, undo, offsets, *, out=None, stream=None):
+    """The gather's gradient: [T, D], each token's kept rows of dxs [T * k, D]
+    summed in float32."""
+    shp = _route_args(dxs, "dxs", True, undo, offsets)
+    with _launching(dxs.device, stream) as st:
+        out = _out(out, "out", dxs.dtype, (undo.shape[0], dxs.shape[1]), dxs)
+        _check(lib().lsh_attn_route_gather_backward(ctypes.byref(shp), _ptr(dxs), _ptr(undo),
+                                                    _ptr(offsets), _ptr(out), st))
+    return out
+
+
+def lsh_attn_route_combine(y, weights, undo, offsets, *, out=None, stream=None):
+    """The experts' rows y [T * k, D] back to their tokens: [T, D], each token's
+    kept rows times weights [T, k] (float32), summed in float32."""
+    shp = _route_args(y, "y", True, undo, offsets)
+    _cuda(weights, "weights", torch.float32, undo.shape, y)
+    with _launching(y.device, stream) as st:
+        out = _out(out, "out", y.dtype, (undo.shape[0], y.shape[1]), y)
+        _check(lib().lsh_attn_route_combine(ctypes.byref(shp), _ptr(y), _ptr(weights), _ptr(undo),
+                                            _ptr(offsets), _ptr(out), st))
+    return out
+
+
+def lsh_attn_route_combine_backward(dout, y, weights, undo, offsets, *, stream=None):
+    """The combine's gradients for dout [T, D].  Returns (dy [T * k, D] in y's
+    dtype, dweights float32 [T, k]), zero for dropped entries."""
+    shp = _route_args(y, "y", True, undo, offsets)
+    _cuda(weights, "weights", torch.float32, undo.shape, y)
+    _cuda(dout, "dout", y.dtype, (undo.shape[0], y.shape[1]), y)
+    with _launching(y.device, stream) as st:
+        dy = torch.empty_like(y)
+        dw = torch.empty_like(weights)
+        _check(lib().lsh_attn_route_combine_backward(ctypes.byref(shp), _ptr(dout), _ptr(y),
+                                                     _ptr(weights), _ptr(undo), _ptr(offsets),
+                                                     _ptr(dy), _ptr(dw), st))
+    return dy, dw

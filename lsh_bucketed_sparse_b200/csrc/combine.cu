@@ -8,47 +8,12 @@
 // rows (coalesced), and out is written the same way.
 #include "common.cuh"
 #include "internal.h"
+#include "vec16.cuh"
 
 namespace lsh {
 namespace {
 
 constexpr int kThreads = 256;
-
-template <typename T> struct Vec16;
-template <> struct Vec16<float> {
-  static constexpr int N = 4;
-  __device__ static uint4 raw(const float* p) { return *reinterpret_cast<const uint4*>(p); }
-  __device__ static void unpack(const uint4& u, float* f) {
-    f[0] = __uint_as_float(u.x); f[1] = __uint_as_float(u.y);
-    f[2] = __uint_as_float(u.z); f[3] = __uint_as_float(u.w);
-  }
-  __device__ static void load(const float* p, float* f) { unpack(raw(p), f); }
-  __device__ static void store(float* p, const float* f) {
-    *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
-  }
-};
-template <> struct Vec16<__nv_bfloat16> {
-  static constexpr int N = 8;
-  __device__ static uint4 raw(const __nv_bfloat16* p) {
-    return *reinterpret_cast<const uint4*>(p);
-  }
-  __device__ static void unpack(const uint4& u, float* f) {
-    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const float2 x = __bfloat1622float2(h[t]);
-      f[2 * t] = x.x; f[2 * t + 1] = x.y;
-    }
-  }
-  __device__ static void load(const __nv_bfloat16* p, float* f) { unpack(raw(p), f); }
-  __device__ static void store(__nv_bfloat16* p, const float* f) {
-    uint4 u;
-    __nv_bfloat162* h = reinterpret_cast<__nv_bfloat162*>(&u);
-#pragma unroll
-    for (int t = 0; t < 4; ++t) h[t] = __floats2bfloat162_rn(f[2 * t], f[2 * t + 1]);
-    *reinterpret_cast<uint4*>(p) = u;
-  }
-};
 
 // NH > 0: the number of rounds as a compile-time constant, so every round's
 // lse and 16-byte piece are loaded before any is used (all loads in flight

@@ -119,4 +119,57 @@ cudaError_t launch_attn_tc(const Problem& p, const void* qk, const void* v, cons
 cudaError_t launch_combine(const Problem& p, const void* o_rounds, const float* lse_rounds,
                            void* out, float* lse, cudaStream_t st);
 
+// ---- stable order of integer keys (key_sort.cu) -------------------------------
+// Keys outside [0, K) come last.  perm[s]: the entry in slot s; undo (may be
+// NULL) its inverse; offsets (may be NULL; K < 1024 only) [K + 1]: each key's
+// first slot, offsets[K] the first slot of the keys outside; with runs (may be
+// NULL), sorted[n] gets the keys in order and runs[K] each key's slots [x, y).
+size_t key_sort_scratch_bytes(long long n, int K);
+cudaError_t launch_key_sort(long long n, int K, const void* keys, bool keys64, int32_t* perm,
+                            int32_t* undo, int32_t* offsets, int32_t* sorted, int2* runs,
+                            void* scratch, cudaStream_t st);
+
+// ---- the token table: lookup, its gradient, cross entropy -----------------------
+// Validated copy of lsh_table.
+struct TableProblem {
+  long long rows;
+  int vocab, d;
+  bool bf16, idx64, portable;
+  float scale;
+  size_t elem() const { return bf16 ? 2 : 4; }
+};
+cudaError_t launch_embed(const TableProblem& p, const void* tokens, const void* table, void* out,
+                         cudaStream_t st);
+size_t embed_backward_workspace_bytes(const TableProblem& p);
+cudaError_t launch_embed_backward(const TableProblem& p, const void* tokens, const void* dout,
+                                  const void* init, void* dtable, void* workspace,
+                                  cudaStream_t st);
+size_t xent_workspace_bytes(const TableProblem& p);
+cudaError_t launch_xent(const TableProblem& p, const void* x, const void* table,
+                        const void* targets, float* loss, float* lse, void* workspace,
+                        cudaStream_t st);
+size_t xent_backward_workspace_bytes(const TableProblem& p);
+cudaError_t launch_xent_backward(const TableProblem& p, const void* x, const void* table,
+                                 const void* targets, const float* lse, const float* dloss,
+                                 void* dx, void* dtable, void* workspace, cudaStream_t st);
+
+// ---- tokens to experts and back (route.cu) ---------------------------------------
+// Validated copy of lsh_route.
+struct RouteProblem {
+  long long tokens;
+  int k, experts, d;
+  bool bf16, idx64;
+  long long entries() const { return tokens * k; }
+};
+cudaError_t launch_route_gather(const RouteProblem& p, const void* x, const int32_t* undo,
+                                const int32_t* offsets, void* xs, cudaStream_t st);
+// weights NULL: every weight 1
+cudaError_t launch_route_combine(const RouteProblem& p, const void* y, const float* weights,
+                                 const int32_t* undo, const int32_t* offsets, void* out,
+                                 cudaStream_t st);
+cudaError_t launch_route_combine_backward(const RouteProblem& p, const void* dout, const void* y,
+                                          const float* weights, const int32_t* undo,
+                                          const int32_t* offsets, void* dy, float* dweights,
+                                          cudaStream_t st);
+
 }  // namespace lsh

@@ -1,0 +1,117 @@
+// Cross entropy over the vocabulary: kernel choice, workspaces, and the last
+// step of the forward (each row's slices joined into lse and loss).
+#include "common.cuh"
+#include "internal.h"
+#include "xent.cuh"
+
+namespace lsh {
+namespace {
+
+constexpr int kThreads = 256;
+
+// lse_i = log sum over the slices, loss_i = lse_i - z_i,t_i.
+template <typename I>
+__global__ void __launch_bounds__(kThreads)
+xent_join_kernel(const float2* __restrict__ part, const float* __restrict__ zt,
+                 const I* __restrict__ targets, float* __restrict__ loss, float* __restrict__ lse,
+                 int rows, int slices, int vocab) {
+  wait_prior_grid();
+  const int row = blockIdx.x * kThreads + threadIdx.x;
+  if (row >= rows) return;
+  float m = -INFINITY, s = 0.f;
+  for (int k = 0; k < slices; ++k) {
+    const float2 p = part[(size_t)k * rows + row];
+    lse_add(m, s, p.x, p.y);
+  }
+  const float l = m + logf(s);
+  lse[row] = l;
+  loss[row] = target_of(targets, row, vocab) >= 0 ? l - zt[row] : 0.f;
+}
+
+__global__ void __launch_bounds__(kThreads) xent_zero_kernel(uint4* out, long long pieces) {
+  wait_prior_grid();
+  const long long p = (long long)blockIdx.x * kThreads + threadIdx.x;
+  if (p < pieces) out[p] = make_uint4(0, 0, 0, 0);
+}
+
+template <typename I>
+__global__ void __launch_bounds__(kThreads)
+xent_clean_kernel(const uint4* __restrict__ x, const I* __restrict__ targets,
+                  uint4* __restrict__ clean, long long pieces, int per_row, int vocab) {
+  wait_prior_grid();
+  const long long p = (long long)blockIdx.x * kThreads + threadIdx.x;
+  if (p >= pieces) return;
+  clean[p] = target_of(targets, p / per_row, vocab) >= 0 ? x[p] : make_uint4(0, 0, 0, 0);
+}
+
+size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+
+int slices_of(const TableProblem& p) { return xent_portable_slices(p); }
+
+}  // namespace
+
+cudaError_t launch_xent_clean(const TableProblem& p, const void* x, const void* targets,
+                              void* clean, cudaStream_t st) {
+  const int per_row = (int)(p.d * p.elem() / 16);
+  const long long pieces = p.rows * per_row;
+  const dim3 grid((unsigned)((pieces + kThreads - 1) / kThreads)), block(kThreads);
+  const uint4* src = static_cast<const uint4*>(x);
+  uint4* dst = static_cast<uint4*>(clean);
+  cudaError_t e =
+      p.idx64 ? launch_dependent(xent_clean_kernel<int64_t>, grid, block, 0, st, src,
+                                 static_cast<const int64_t*>(targets), dst, pieces, per_row, p.vocab)
+              : launch_dependent(xent_clean_kernel<int32_t>, grid, block, 0, st, src,
+                                 static_cast<const int32_t*>(targets), dst, pieces, per_row, p.vocab);
+  if (e == cudaSuccess) note_launch();
+  return e;
+}
+
+size_t xent_workspace_bytes(const TableProblem& p) {
+  if (p.rows == 0) return 0;
+  return align256((size_t)p.rows * slices_of(p) * sizeof(float2)) +
+         align256((size_t)p.rows * sizeof(float));
+}
+
+cudaError_t launch_xent(const TableProblem& p, const void* x, const void* table,
+                        const void* targets, float* loss, float* lse, void* workspace,
+                        cudaStream_t st) {
+  if (p.rows == 0) return cudaSuccess;
+  const int slices = slices_of(p), rows = (int)p.rows;
+  float2* part = static_cast<float2*>(workspace);
+  float* zt = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                       align256((size_t)p.rows * slices * sizeof(float2)));
+  cudaError_t e = launch_xent_portable(p, x, table, targets, part, zt, st);
+  if (e) return e;
+  const dim3 grid((rows + kThreads - 1) / kThreads), block(kThreads);
+  e = p.idx64 ? launch_dependent(xent_join_kernel<int64_t>, grid, block, 0, st,
+                                 static_cast<const float2*>(part), static_cast<const float*>(zt),
+                                 static_cast<const int64_t*>(targets), loss, lse, rows, slices,
+                                 p.vocab)
+              : launch_dependent(xent_join_kernel<int32_t>, grid, block, 0, st,
+                                 static_cast<const float2*>(part), static_cast<const float*>(zt),
+                                 static_cast<const int32_t*>(targets), loss, lse, rows, slices,
+                                 p.vocab);
+  if (e == cudaSuccess) note_launch();
+  return e;
+}
+
+size_t xent_backward_workspace_bytes(const TableProblem& p) {
+  return p.rows ? xent_portable_backward_bytes(p) : 0;
+}
+
+cudaError_t launch_xent_backward(const TableProblem& p, const void* x, const void* table,
+                                 const void* targets, const float* lse, const float* dloss,
+                                 void* dx, void* dtable, void* workspace, cudaStream_t st) {
+  if (p.rows == 0) {  // no tokens: the table's gradient is zero
+    const long long pieces = (long long)p.vocab * p.d * (long long)p.elem() / 16;
+    cudaError_t e = launch_dependent(xent_zero_kernel,
+                                     dim3((unsigned)((pieces + kThreads - 1) / kThreads)),
+                                     dim3(kThreads), 0, st, static_cast<uint4*>(dtable), pieces);
+    if (e == cudaSuccess) note_launch();
+    return e;
+  }
+  return launch_xent_portable_backward(p, x, table, targets, lse, dloss, dx, dtable, workspace,
+                                       st);
+}
+
+}  // namespace lsh

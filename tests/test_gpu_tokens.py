@@ -1,0 +1,490 @@
+"""Token table, cross entropy and routing on the GPU against float64 torch
+(tokens_ref.py has the formulas and the bounds)."""
+
+import ctypes
+import math
+
+import pytest
+import torch
+
+import lsh_bucketed_sparse_b200 as lsh
+import tokens_ref as R
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+def gen(seed):
+    return torch.Generator(DEV).manual_seed(seed)
+
+
+def randn(g, *shape, dtype=F32, scale=1.0):
+    return (torch.randn(*shape, device=DEV, generator=g) * scale).to(dtype)
+
+
+def make_tokens(g, n, vocab, index, skew=0.0, holes=0.0):
+    """Ids in [0, vocab); a share `skew` is one id, a share `holes` outside."""
+    t = torch.randint(0, vocab, (n,), device=DEV, generator=g)
+    u = torch.rand(n, device=DEV, generator=g)
+    t = torch.where(u < skew, torch.full_like(t, vocab // 2), t)
+    out = torch.where(torch.rand(n, device=DEV, generator=g) < 0.5, torch.full_like(t, -1),
+                      torch.full_like(t, vocab))
+    return torch.where(u > 1 - holes, out, t).to(index)
+
+
+# ---- token table ---------------------------------------------------------------
+EMBED = [  # rows, vocab, d, dtype, index, scale
+    (0, 16, 8, BF16, torch.int64, 1.0),
+    (1, 1, 8, F32, torch.int32, 2.0),
+    (8, 1000, 512, BF16, torch.int64, math.sqrt(512)),
+    (257, 50, 24, BF16, torch.int32, 0.5),
+    (1000, 33, 1032, F32, torch.int64, 1.0),
+    (3, 20, 16384, BF16, torch.int64, 1.0),
+]
+
+
+@pytest.mark.parametrize("n,vocab,d,dtype,index,scale", EMBED)
+def test_embed(n, vocab, d, dtype, index, scale):
+    g = gen(n + vocab)
+    tok = make_tokens(g, n, vocab, index, holes=0.2)
+    table = randn(g, vocab, d, dtype=dtype)
+    R.check("out", lsh.lsh_attn_embed(tok, table, scale=scale), R.embed(tok, table, scale))
+
+
+EMBED_BWD = [  # rows, vocab, d, dtype, index, skew, holes
+    (0, 16, 8, BF16, torch.int64, 0, 0),
+    (1, 1, 8, F32, torch.int32, 0, 0),
+    (1, 300, 16, BF16, torch.int64, 0, 1.0),       # nothing but padding
+    (64, 4, 40, BF16, torch.int32, 1.0, 0),        # one run as long as a chunk
+    (65, 4, 40, F32, torch.int64, 1.0, 0),         # one longer
+    (1000, 7, 72, BF16, torch.int64, 0, 0.1),
+    (2047, 1023, 136, F32, torch.int32, 0.3, 0.1),
+    (2048, 1024, 8, BF16, torch.int64, 0.5, 0),    # the first size of two digits
+    (6000, 50021, 24, F32, torch.int64, 0.2, 0.2),
+    (5000, 1 << 20, 8, BF16, torch.int32, 0.1, 0.1),
+    (20000, 300, 264, BF16, torch.int64, 0.9, 0),
+    (300, 10, 16384, F32, torch.int64, 0.5, 0),
+]
+
+
+@pytest.mark.parametrize("into", [False, True])
+@pytest.mark.parametrize("n,vocab,d,dtype,index,skew,holes", EMBED_BWD)
+def test_embed_backward(n, vocab, d, dtype, index, skew, holes, into):
+    g = gen(n * 3 + vocab)
+    tok = make_tokens(g, n, vocab, index, skew, holes)
+    dout = randn(g, n, d, dtype=dtype)
+    init = randn(g, vocab, d, dtype=dtype) if into else None
+    want = R.embed_backward(tok, dout, vocab, 0.75, init)
+    got = lsh.lsh_attn_embed_backward(tok, dout, vocab, scale=0.75, init=init)
+    R.check("dtable", got, want)
+    # the same bits again, and added in place
+    again = lsh.lsh_attn_embed_backward(tok, dout, vocab, scale=0.75, init=init,
+                                        out=init if into else None)
+    assert torch.equal(got, again)
+
+
+def test_embed_takes_any_leading_shape_and_a_slice_of_tokens():
+    g = gen(5)
+    ids = torch.randint(0, 40, (2 * 3 * 5 + 1,), device=DEV, generator=g)
+    tok, table = ids[1:].view(2, 3, 5), randn(g, 40, 16)     # 8 bytes off a 16-byte address
+    out = lsh.lsh_attn_embed(tok, table)
+    assert out.shape == (2, 3, 5, 16)
+    assert torch.equal(out, table[tok])
+    dt = lsh.lsh_attn_embed_backward(tok, out, 40)
+    R.check("dtable", dt, R.embed_backward(tok, out, 40, 1.0))
+
+
+def test_tokens_far_outside_the_table_are_padding():
+    # int64 ids whose low 32 bits are a valid id
+    tok = torch.tensor([3, 3 + (1 << 32), -(1 << 40) + 3, (1 << 62), 7], device=DEV)
+    table = randn(gen(1), 8, 8)
+    want = table[torch.tensor([3, 0, 0, 0, 7], device=DEV)]
+    want[1:4] = 0
+    assert torch.equal(lsh.lsh_attn_embed(tok, table), want)
+    dt = lsh.lsh_attn_embed_backward(tok, torch.ones(5, 8, device=DEV), 8)
+    assert dt.sum() == 16 and dt[3, 0] == 1 and dt[7, 0] == 1
+    loss, lse = lsh.lsh_attn_xent(want, table, tok)
+    assert torch.equal(loss == 0, torch.tensor([0, 1, 1, 1, 0], device=DEV).bool())
+    assert bool(torch.isfinite(lse).all())
+
+
+# ---- cross entropy ---------------------------------------------------------------
+XENT = [  # rows, vocab, d, dtype, index, scale, holes
+    (1, 1, 8, BF16, torch.int64, 1.0, 0),
+    (1, 2, 8, F32, torch.int32, 1.0, 0),
+    (5, 1000, 64, BF16, torch.int32, 1.0, 0),
+    (128, 256, 64, BF16, torch.int64, 1.0, 0),
+    (129, 257, 72, BF16, torch.int64, 0.125, 0.3),
+    (256, 255, 128, F32, torch.int32, 1.0, 0),
+    (255, 513, 520, BF16, torch.int32, 1.0, 0.1),
+    (300, 777, 136, F32, torch.int64, -0.5, 0.5),
+    (513, 2049, 264, BF16, torch.int64, 1.0, 1.0),  # nothing but padding
+    (700, 5000, 64, BF16, torch.int64, 1.0, 0.05),
+    (1025, 3001, 40, F32, torch.int64, 1.0, 0.1),
+    (33, 20011, 24, BF16, torch.int64, 1.0, 0),
+]
+
+
+def make_xent(n, vocab, d, dtype, index, holes, seed=0):
+    """Rows that lean to their targets by 0 to 10, as a trained model's."""
+    g = gen(n * 7 + vocab + seed)
+    t = make_tokens(g, n, vocab, index, 0.1, holes)
+    table = randn(g, vocab, d, scale=d ** -0.5)
+    lift = 10 * torch.rand(n, 1, device=DEV, generator=g)
+    x = randn(g, n, d) + lift * table[t.long().clamp(0, vocab - 1)]
+    return x.to(dtype), table.to(dtype), t, randn(g, n)
+
+
+@pytest.mark.parametrize("portable", [False, True])
+@pytest.mark.parametrize("n,vocab,d,dtype,index,scale,holes", XENT)
+def test_xent(n, vocab, d, dtype, index, scale, holes, portable):
+    x, table, t, dloss = make_xent(n, vocab, d, dtype, index, holes)
+    loss, lse = lsh.lsh_attn_xent(x, table, t, scale=scale, portable=portable)
+    want_loss, want_lse = R.xent(x, table, t, scale)
+    R.check("lse", lse, want_lse)
+    R.check("loss", loss, want_loss)
+    dx, dw = lsh.lsh_attn_xent_backward(x, table, t, lse, dloss, scale=scale, portable=portable)
+    lsh.lsh_attn_device_check()
+    want_dx, want_dw = R.xent_backward(x, table, t, dloss, scale,
+                                       BF16 if dtype == BF16 and not portable else None)
+    R.check("dx", dx, want_dx)
+    R.check("dtable", dw, want_dw)
+    # the same inputs give the same bits
+    again = lsh.lsh_attn_xent_backward(x, table, t, lse, dloss, scale=scale, portable=portable)
+    assert torch.equal(again[0], dx) and torch.equal(again[1], dw)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_xent_of_no_rows(dtype):
+    x, table = torch.empty(0, 16, device=DEV, dtype=dtype), randn(gen(0), 9, 16, dtype=dtype)
+    t, f = torch.empty(0, device=DEV, dtype=torch.int64), torch.empty(0, device=DEV)
+    loss, lse = lsh.lsh_attn_xent(x, table, t)
+    assert loss.shape == lse.shape == (0,)
+    dx, dw = lsh.lsh_attn_xent_backward(x, table, t, f, f)
+    assert dx.shape == (0, 16) and not bool(dw.any())
+
+
+@pytest.mark.parametrize("portable", [False, True])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_padding_rows_may_hold_anything(dtype, portable):
+    x, table, t, dloss = make_xent(300, 400, 64, dtype, torch.int64, 0.3)
+    pad = (t < 0) | (t >= 400)
+    assert bool(pad.any())
+    bad, up = x.clone(), dloss.clone()
+    bad[pad] = float("nan")
+    up[pad] = float("inf")
+    loss, lse = lsh.lsh_attn_xent(bad, table, t, portable=portable)
+    (want, bound), (want_lse, lse_bound) = R.xent(x, table, t, 1.0)
+    assert not bool(loss[pad].any())
+    R.check("loss", loss[~pad], (want[~pad], bound[~pad]))
+    R.check("lse", lse[~pad], (want_lse[~pad], lse_bound[~pad]))
+    dx, dw = lsh.lsh_attn_xent_backward(bad, table, t, lse, up, portable=portable)
+    assert not bool(dx[pad].any())
+    want_dx, want_dw = R.xent_backward(x, table, t, dloss, 1.0,
+                                       BF16 if dtype == BF16 and not portable else None)
+    R.check("dx", dx[~pad], (want_dx[0][~pad], want_dx[1][~pad]))
+    R.check("dtable", dw, want_dw)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_far_logits_do_not_overflow(dtype):
+    # logits of some +-12000: exp of any of them alone is 0 or infinite
+    g = gen(11)
+    x, table = randn(g, 130, 64, dtype=dtype, scale=8), randn(g, 300, 64, dtype=dtype, scale=8)
+    t = torch.randint(0, 300, (130,), device=DEV, generator=g)
+    loss, lse = lsh.lsh_attn_xent(x, table, t, scale=4.0)
+    want_loss, want_lse = R.xent(x, table, t, 4.0)
+    assert float(want_lse[0].max()) > 5000
+    R.check("lse", lse, want_lse)
+    R.check("loss", loss, want_loss)
+    dx, dw = lsh.lsh_attn_xent_backward(x, table, t, lse, torch.ones(130, device=DEV), scale=4.0)
+    assert bool(torch.isfinite(dx.float()).all()) and bool(torch.isfinite(dw.float()).all())
+
+
+def test_words_at_minus_infinity_take_no_part():
+    # a word that is ruled out by a logit of -inf: probability and gradient 0
+    g = gen(12)
+    x = randn(g, 40, 16).abs()
+    table = randn(g, 50, 16)
+    table[10:20, 3] = -float("inf")
+    t = torch.randint(20, 50, (40,), device=DEV, generator=g)
+    loss, lse = lsh.lsh_attn_xent(x, table, t, portable=True)
+    keep = torch.cat([torch.arange(10), torch.arange(20, 50)]).to(DEV)
+    (want, bound), (want_lse, lse_bound) = R.xent(x, table[keep], t - 10, 1.0)
+    R.check("lse", lse, (want_lse, lse_bound))
+    R.check("loss", loss, (want, bound))
+
+
+def test_a_nan_in_a_row_stays_in_that_row():
+    x, table, t, dloss = make_xent(200, 300, 64, BF16, torch.int64, 0)
+    x[7, 3] = float("nan")
+    loss, lse = lsh.lsh_attn_xent(x, table, t)
+    assert bool(torch.isnan(lse[7])) and bool(torch.isnan(loss[7]))
+    others = torch.arange(200, device=DEV) != 7
+    assert bool(torch.isfinite(lse[others]).all())
+    dx, _ = lsh.lsh_attn_xent_backward(x, table, t, lse, dloss)
+    assert bool(torch.isnan(dx[7].float()).any())
+    assert bool(torch.isfinite(dx[others].float()).all())
+
+
+@pytest.mark.parametrize("portable", [False, True])
+def test_xent_gradient_against_differences(portable):
+    # float64 central differences of the definition along random directions
+    x, table, t, dloss = make_xent(150, 270, 48, F32, torch.int64, 0.2, seed=3)
+    lse = lsh.lsh_attn_xent(x, table, t, scale=0.7, portable=portable)[1]
+    dx, dw = lsh.lsh_attn_xent_backward(x, table, t, lse, dloss, scale=0.7, portable=portable)
+    g = gen(99)
+    ux, uw = randn(g, *x.shape).double(), randn(g, *table.shape).double()
+
+    def f(h):
+        loss = R.xent(x.double() + h * ux, table.double() + h * uw, t, 0.7)[0][0]
+        return float((loss * dloss.double()).sum())
+
+    # third-order error of the differences: with h = 1e-4 relative 1e-8 of sums
+    # of the order of their terms; the gradient's own bound on top
+    slope = (f(1e-4) - f(-1e-4)) / 2e-4
+    mine = float((dx.double() * ux).sum() + (dw.double() * uw).sum())
+    want_dx, want_dw = R.xent_backward(x, table, t, dloss, 0.7)
+    size = float((want_dx[0] * ux).abs().sum() + (want_dw[0] * uw).abs().sum())
+    bound = float((want_dx[1] * ux.abs()).sum() + (want_dw[1] * uw.abs()).sum()) + 1e-6 * size
+    assert abs(slope - mine) <= bound
+
+
+# ---- routing ---------------------------------------------------------------------
+ROUTE = [  # tokens, k, experts, d, dtype, index, dropped
+    (0, 2, 4, 16, BF16, torch.int64, 0),
+    (1, 1, 1, 8, F32, torch.int32, 0),
+    (64, 2, 8, 512, BF16, torch.int64, 0),
+    (100, 1, 5, 40, F32, torch.int64, 1.0),           # every entry dropped
+    (1000, 4, 1023, 72, BF16, torch.int32, 0.1),
+    (341, 6, 160, 264, F32, torch.int32, 0.3),
+    (1025, 2, 64, 1032, BF16, torch.int64, 0.02),
+    (3000, 64, 70, 8, BF16, torch.int64, 0.05),
+    (2049, 8, 256, 128, F32, torch.int64, 0),
+    (5, 3, 2, 16384, BF16, torch.int32, 0.2),
+]
+
+
+@pytest.mark.parametrize("T,k,E,d,dtype,index,dropped", ROUTE)
+def test_route(T, k, E, d, dtype, index, dropped):
+    g = gen(T + k * 31 + E)
+    ids = make_tokens(g, T * k, E, index, 0.2, dropped).view(T, k)
+    w = torch.rand(T, k, device=DEV, generator=g)
+    perm, undo, offsets = lsh.lsh_attn_route_sort(ids, E)
+    for name, got, want in zip(("perm", "undo", "offsets"), (perm, undo, offsets),
+                               R.route_plan(ids.cpu(), E)):
+        assert torch.equal(got.cpu(), want), name
+    kept = int(offsets[-1])
+    x, y = randn(g, T, d, dtype=dtype), randn(g, T * k, d, dtype=dtype)
+    # rows and weights of dropped entries are never read
+    y[kept:] = float("nan")
+    w = torch.where(undo < kept, w, torch.full_like(w, float("nan")))
+    assert torch.equal(lsh.lsh_attn_route_gather(x, undo, offsets), R.route_gather(x, undo, kept))
+    R.check("out", lsh.lsh_attn_route_combine(y, w, undo, offsets),
+            R.route_combine(y, w, undo, kept))
+    R.check("dx", lsh.lsh_attn_route_gather_backward(y, undo, offsets),
+            R.route_combine(y, None, undo, kept))
+    dout = randn(g, T, d, dtype=dtype)
+    dy, dw = lsh.lsh_attn_route_combine_backward(dout, y, w, undo, offsets)
+    want_dy, want_dw = R.route_combine_backward(dout, y, w, undo, kept)
+    R.check("dy", dy, want_dy)
+    R.check("dweights", dw, want_dw)
+
+
+def test_an_expert_named_twice_by_one_token():
+    ids = torch.tensor([[2, 2], [0, 2], [1, 1]], device=DEV)
+    perm, undo, offsets = lsh.lsh_attn_route_sort(ids, 3)
+    assert perm.tolist() == [2, 4, 5, 0, 1, 3]
+    assert offsets.tolist() == [0, 1, 3, 6]
+    x = randn(gen(2), 3, 8)
+    xs = lsh.lsh_attn_route_gather(x, undo, offsets)
+    assert torch.equal(xs, x[perm.long() // 2])
+    assert torch.equal(lsh.lsh_attn_route_gather_backward(xs, undo, offsets), 2 * x)
+
+
+# ---- streams, graphs, several calls ------------------------------------------------
+def _step(tok, table, targets, ids, w):
+    """Tokens in, routed copies, loss against the same table, every gradient."""
+    h = lsh.lsh_attn_embed(tok, table, scale=2.0)
+    _, undo, off = lsh.lsh_attn_route_sort(ids, 8)
+    xs = lsh.lsh_attn_route_gather(h, undo, off)
+    x = lsh.lsh_attn_route_combine(xs, w, undo, off)
+    loss, lse = lsh.lsh_attn_xent(x, table, targets)
+    dloss = (targets >= 0).float() / targets.numel()
+    dx, dw_table = lsh.lsh_attn_xent_backward(x, table, targets, lse, dloss)
+    dxs, dweights = lsh.lsh_attn_route_combine_backward(dx, xs, w, undo, off)
+    dh = lsh.lsh_attn_route_gather_backward(dxs, undo, off)
+    dtable = lsh.lsh_attn_embed_backward(tok, dh, table.shape[0], scale=2.0, init=dw_table,
+                                         out=dw_table)
+    return loss, dweights, dtable
+
+
+def _step_inputs(seed, dtype, n=333, vocab=600, d=64):
+    g = gen(seed)
+    tok = make_tokens(g, n, vocab, torch.int64, 0.3, 0.05)
+    table = randn(g, vocab, d, dtype=dtype, scale=d ** -0.5)
+    ids = make_tokens(g, n * 2, 8, torch.int64, 0, 0.1).view(n, 2)
+    return tok, table, make_tokens(g, n, vocab, torch.int64, 0.1, 0.1), ids, \
+        torch.rand(n, 2, device=DEV, generator=g)
+
+
+def test_a_step_against_float64_autograd():
+    tok, table, targets, ids, w = _step_inputs(0, F32)
+    loss, dweights, dtable = _step(tok, table, targets, ids, w)
+    lsh.lsh_attn_device_check()
+    V, D = table.shape
+    t64, w64 = table.double().requires_grad_(), w.double().requires_grad_()
+    pad = torch.cat([t64, torch.zeros(1, D, device=DEV, dtype=torch.float64)])
+    h = 2.0 * pad[torch.where((tok >= 0) & (tok < V), tok, V)]
+    kept = (ids >= 0) & (ids < 8)
+    x = (torch.where(kept, w64, torch.zeros_like(w64))[..., None] * h[:, None]).sum(1)
+    z = x @ t64.T
+    valid = (targets >= 0) & (targets < V)
+    zt = z.gather(1, torch.where(valid, targets, 0)[:, None])[:, 0]
+    want = torch.where(valid, torch.logsumexp(z, 1) - zt, 0.0)
+    up = ((targets >= 0).double() / targets.numel())
+    (want * up).sum().backward()
+    # float32 throughout: sums of up to n = 333 or V = 600 terms at every step
+    # of a chain of seven, each of relative error 2 * 600 * 2^-24 of magnitudes
+    # that stand within 2^3 of the largest result
+    tol = 7 * 8 * 2 * 600 * 2.0 ** -24
+    for name, got, ref in (("loss", loss, want.detach()), ("dweights", dweights, w64.grad),
+                           ("dtable", dtable, t64.grad)):
+        err = float((got.detach().double() - ref).abs().max() / ref.abs().max())
+        assert err <= tol, f"{name}: {err:.3e} > {tol:.3e}"
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_a_step_captured_and_replayed_on_new_inputs(dtype):
+    a, b = _step_inputs(1, dtype), _step_inputs(2, dtype)
+    want_a, want_b = _step(*a), _step(*b)
+    held = [t.clone() for t in a]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = _step(*held)
+    for inputs, want in ((a, want_a), (b, want_b), (a, want_a)):
+        for h, t in zip(held, inputs):
+            h.copy_(t)
+        graph.replay()
+        for x, y in zip(got, want):
+            assert torch.equal(x, y)
+    lsh.lsh_attn_device_check()
+
+
+def test_calls_on_another_stream():
+    inputs = _step_inputs(4, BF16)
+    want = _step(*inputs)
+    tok, table, targets, ids, w = inputs
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        got = _step(*inputs)
+    # and with the stream handed over
+    out = lsh.lsh_attn_embed(tok, table, scale=2.0, stream=s)
+    perm = lsh.lsh_attn_route_sort(ids, 8, stream=s)[0]
+    loss, lse = lsh.lsh_attn_xent(out, table, targets, stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    for x, y in zip(got, want):
+        assert torch.equal(x, y)
+    assert torch.equal(out, lsh.lsh_attn_embed(tok, table, scale=2.0))
+    assert torch.equal(perm, lsh.lsh_attn_route_sort(ids, 8)[0])
+    assert torch.equal(loss, lsh.lsh_attn_xent(out, table, targets)[0])
+
+
+def test_two_streams_at_once():
+    a, b = _step_inputs(5, BF16, n=3001), _step_inputs(6, BF16, n=2500)
+    want_a, want_b = _step(*a), _step(*b)
+    sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        with torch.cuda.stream(sa):
+            got_a = _step(*a)
+        with torch.cuda.stream(sb):
+            got_b = _step(*b)
+    torch.cuda.synchronize()
+    for x, y in zip(got_a + got_b, want_a + want_b):
+        assert torch.equal(x, y)
+
+
+def test_nothing_is_written_past_the_ends():
+    # outputs inside larger buffers whose borders keep their value
+    g = gen(8)
+    n, V, d = 130, 259, 72
+    tok = make_tokens(g, n, V, torch.int64, 0.6, 0.1)
+    x, table = randn(g, n, d, dtype=BF16), randn(g, V, d, dtype=BF16)
+
+    def framed(rows, cols, dtype):
+        buf = torch.full((rows * cols + 2048,), 7, dtype=dtype, device=DEV)
+        return buf, buf[1024:1024 + rows * cols].view(rows, cols)
+
+    def whole(buf, size):
+        return bool((buf[:1024] == 7).all()) and bool((buf[1024 + size:] == 7).all())
+
+    buf, out = framed(n, d, BF16)
+    lsh.lsh_attn_embed(tok, table, out=out)
+    assert whole(buf, n * d)
+    buf, out = framed(V, d, BF16)
+    lsh.lsh_attn_embed_backward(tok, x, V, out=out)
+    assert whole(buf, V * d)
+    # cross entropy and its gradients through the C ABI, workspaces framed too
+    L, st = lsh.lib(), ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    for portable in (False, True):
+        s = lsh.make_table_shape(n, V, d, BF16, lsh.I64, 1.0, portable)
+        ref = ctypes.byref(s)
+        bl, loss = framed(1, n, F32)
+        be, lse = framed(1, n, F32)
+        need = lsh.lsh_attn_xent_workspace_size(s)
+        bw, ws = framed(1, need, torch.uint8)
+        assert L.lsh_attn_xent(ref, lsh._ptr(x), lsh._ptr(table), lsh._ptr(tok), lsh._ptr(loss),
+                               lsh._ptr(lse), lsh._ptr(ws), need, st) == 0
+        assert whole(bl, n) and whole(be, n) and whole(bw, need)
+        up = torch.ones(n, device=DEV)
+        bx, dx = framed(n, d, BF16)
+        bt, dt = framed(V, d, BF16)
+        need = lsh.lsh_attn_xent_backward_workspace_size(s)
+        bw, ws = framed(1, need, torch.uint8)
+        assert L.lsh_attn_xent_backward(ref, lsh._ptr(x), lsh._ptr(table), lsh._ptr(tok),
+                                        lsh._ptr(lse), lsh._ptr(up), lsh._ptr(dx), lsh._ptr(dt),
+                                        lsh._ptr(ws), need, st) == 0
+        assert whole(bx, n * d) and whole(bt, V * d) and whole(bw, need)
+
+
+def test_binding_checks_its_tensors():
+    tok = torch.zeros(4, dtype=torch.int64, device=DEV)
+    table = torch.zeros(8, 16, device=DEV)
+    x = torch.zeros(4, 16, device=DEV)
+    f = torch.zeros(4, device=DEV)
+    with pytest.raises(TypeError, match="int32 or int64"):
+        lsh.lsh_attn_embed(tok.short(), table)
+    with pytest.raises(TypeError, match="float32 or bfloat16"):
+        lsh.lsh_attn_embed(tok, table.half())
+    with pytest.raises(ValueError, match="vocab"):
+        lsh.lsh_attn_embed(tok, table[0])
+    with pytest.raises(ValueError, match="contiguous"):
+        lsh.lsh_attn_embed(tok, table.T)
+    with pytest.raises(ValueError, match="out must have shape"):
+        lsh.lsh_attn_embed(tok, table, out=x[:2])
+    with pytest.raises(ValueError, match="dout must be"):
+        lsh.lsh_attn_embed_backward(tok, x[:3], 8)
+    with pytest.raises(ValueError, match="init must have shape"):
+        lsh.lsh_attn_embed_backward(tok, x, 8, init=x)
+    with pytest.raises(TypeError, match="table must be"):
+        lsh.lsh_attn_xent(x, table.bfloat16(), tok)
+    with pytest.raises(ValueError, match="targets must have shape"):
+        lsh.lsh_attn_xent(x, table, tok[:3])
+    with pytest.raises(TypeError, match="lse must be"):
+        lsh.lsh_attn_xent_backward(x, table, tok, f.double(), f)
+    with pytest.raises(TypeError, match="workspace must be"):
+        lsh.lsh_attn_xent(x, table, tok, workspace=f)
+    with pytest.raises(lsh.LshError, match="LSH_ERR_WORKSPACE"):
+        lsh.lsh_attn_xent(x, table, tok, workspace=torch.empty(1, dtype=torch.uint8, device=DEV))
+    with pytest.raises(lsh.LshError, match="multiple of 8"):
+        lsh.lsh_attn_embed(tok, torch.zeros(8, 12, device=DEV))
+    with pytest.raises(ValueError, match="undo must be"):
+        lsh.lsh_attn_route_gather(x, tok.int(), tok.int())
+    with pytest.raises(ValueError, match=r"y must be \[8, d_model\]"):
+        lsh.lsh_attn_route_combine(x, torch.zeros(4, 2, device=DEV),
+                                   torch.zeros(4, 2, dtype=torch.int32, device=DEV), tok.int())
+    with pytest.raises(ValueError, match="stream is on|CUDA"):
+        lsh.lsh_attn_embed(tok.cpu(), table)
