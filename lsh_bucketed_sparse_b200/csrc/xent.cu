@@ -9,23 +9,35 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// lse_i = log sum over the slices, loss_i = lse_i - z_i,t_i.
+// lse_i = log sum over the slices, loss_i = lse_i - z_i,t_i.  A block joins 32
+// rows: each warp every kJoinWarps-th slice, then the warps in order.
+constexpr int kJoinWarps = kThreads / 32;
 template <typename I>
 __global__ void __launch_bounds__(kThreads)
 xent_join_kernel(const float2* __restrict__ part, const float* __restrict__ zt,
                  const I* __restrict__ targets, float* __restrict__ loss, float* __restrict__ lse,
                  int rows, int slices, int vocab) {
+  __shared__ float2 sums[kJoinWarps][32];
   wait_prior_grid();
-  const int row = blockIdx.x * kThreads + threadIdx.x;
-  if (row >= rows) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = blockIdx.x * 32 + lane;
   float m = -INFINITY, s = 0.f;
-  for (int k = 0; k < slices; ++k) {
-    const float2 p = part[(size_t)k * rows + row];
-    lse_add(m, s, p.x, p.y);
+  if (row < rows) {
+#pragma unroll 4
+    for (int k = warp; k < slices; k += kJoinWarps) {
+      const float2 p = part[(size_t)k * rows + row];
+      lse_add(m, s, p.x, p.y);
+    }
   }
-  const float l = m + logf(s);
-  lse[row] = l;
-  loss[row] = target_of(targets, row, vocab) >= 0 ? l - zt[row] : 0.f;
+  sums[warp][lane] = make_float2(m, s);
+  __syncthreads();
+  if (warp != 0 || row >= rows) return;
+#pragma unroll
+  for (int w = 1; w < kJoinWarps; ++w) lse_add(m, s, sums[w][lane].x, sums[w][lane].y);
+  const float log_s = log2f(s);
+  lse[row] = (m + log_s) * kLn2;
+  // the target's logit next to the maximum first: they may be the same
+  loss[row] = target_of(targets, row, vocab) >= 0 ? ((m - zt[row]) + log_s) * kLn2 : 0.f;
 }
 
 __global__ void __launch_bounds__(kThreads) xent_zero_kernel(uint4* out, long long pieces) {
@@ -46,7 +58,9 @@ xent_clean_kernel(const uint4* __restrict__ x, const I* __restrict__ targets,
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
-int slices_of(const TableProblem& p) { return xent_portable_slices(p); }
+int slices_of(const TableProblem& p) {
+  return xent_tc_supported(p) ? xent_tc_slices(p) : xent_portable_slices(p);
+}
 
 }  // namespace
 
@@ -69,7 +83,8 @@ cudaError_t launch_xent_clean(const TableProblem& p, const void* x, const void* 
 size_t xent_workspace_bytes(const TableProblem& p) {
   if (p.rows == 0) return 0;
   return align256((size_t)p.rows * slices_of(p) * sizeof(float2)) +
-         align256((size_t)p.rows * sizeof(float));
+         align256((size_t)p.rows * sizeof(float)) +
+         (xent_tc_supported(p) ? xent_tc_bytes(p) : 0);
 }
 
 cudaError_t launch_xent(const TableProblem& p, const void* x, const void* table,
@@ -80,9 +95,12 @@ cudaError_t launch_xent(const TableProblem& p, const void* x, const void* table,
   float2* part = static_cast<float2*>(workspace);
   float* zt = reinterpret_cast<float*>(static_cast<char*>(workspace) +
                                        align256((size_t)p.rows * slices * sizeof(float2)));
-  cudaError_t e = launch_xent_portable(p, x, table, targets, part, zt, st);
+  void* scratch = reinterpret_cast<char*>(zt) + align256((size_t)p.rows * sizeof(float));
+  cudaError_t e = xent_tc_supported(p)
+                      ? launch_xent_tc(p, x, table, targets, part, zt, scratch, st)
+                      : launch_xent_portable(p, x, table, targets, part, zt, st);
   if (e) return e;
-  const dim3 grid((rows + kThreads - 1) / kThreads), block(kThreads);
+  const dim3 grid((rows + 31) / 32), block(kThreads);
   e = p.idx64 ? launch_dependent(xent_join_kernel<int64_t>, grid, block, 0, st,
                                  static_cast<const float2*>(part), static_cast<const float*>(zt),
                                  static_cast<const int64_t*>(targets), loss, lse, rows, slices,
@@ -96,7 +114,8 @@ cudaError_t launch_xent(const TableProblem& p, const void* x, const void* table,
 }
 
 size_t xent_backward_workspace_bytes(const TableProblem& p) {
-  return p.rows ? xent_portable_backward_bytes(p) : 0;
+  if (p.rows == 0) return 0;
+  return xent_tc_supported(p) ? xent_tc_backward_bytes(p) : xent_portable_backward_bytes(p);
 }
 
 cudaError_t launch_xent_backward(const TableProblem& p, const void* x, const void* table,
@@ -110,8 +129,10 @@ cudaError_t launch_xent_backward(const TableProblem& p, const void* x, const voi
     if (e == cudaSuccess) note_launch();
     return e;
   }
-  return launch_xent_portable_backward(p, x, table, targets, lse, dloss, dx, dtable, workspace,
-                                       st);
+  return xent_tc_supported(p) ? launch_xent_tc_backward(p, x, table, targets, lse, dloss, dx,
+                                                        dtable, workspace, st)
+                              : launch_xent_portable_backward(p, x, table, targets, lse, dloss,
+                                                              dx, dtable, workspace, st);
 }
 
 }  // namespace lsh

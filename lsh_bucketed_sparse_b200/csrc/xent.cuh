@@ -15,11 +15,14 @@ __device__ __forceinline__ int target_of(const I* targets, long long row, int vo
   return t >= 0 && t < (I)vocab ? (int)t : -1;
 }
 
-// (m, s) stands for s exp(m); adds (m2, s2).  A NaN goes into the sum.
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+
+// The forward's logits are in units of log2: (m, s) stands for s 2^m.  Adds
+// (m2, s2).  A NaN goes into the sum.
 __device__ __forceinline__ void lse_add(float& m, float& s, float m2, float s2) {
   const float top = fmaxf(m, m2);
-  const float ref = top == -INFINITY ? 0.f : top;  // nothing but exp(-inf) so far
-  s = s * expf(m - ref) + s2 * expf(m2 - ref);
+  const float ref = top == -INFINITY ? 0.f : top;  // nothing but 2^-inf so far
+  s = s * exp2f(m - ref) + s2 * exp2f(m2 - ref);
   m = top;
 }
 
@@ -28,9 +31,22 @@ __device__ __forceinline__ void lse_add(float& m, float& s, float m2, float s2) 
 cudaError_t launch_xent_clean(const TableProblem& p, const void* x, const void* targets,
                               void* clean, cudaStream_t st);
 
+// Forward, of either kind: part[slice][row] = (maximum, sum) over the slice's
+// logits, zt[row] the target's logit where the row has a target, in log2.
+
+// ---- tensor cores (xent_tc.cu) ---------------------------------------------------
+bool xent_tc_supported(const TableProblem& p);
+int xent_tc_slices(const TableProblem& p);
+size_t xent_tc_bytes(const TableProblem& p);  // of scratch
+cudaError_t launch_xent_tc(const TableProblem& p, const void* x, const void* table,
+                           const void* targets, float2* part, float* zt, void* scratch,
+                           cudaStream_t st);
+size_t xent_tc_backward_bytes(const TableProblem& p);
+cudaError_t launch_xent_tc_backward(const TableProblem& p, const void* x, const void* table,
+                                    const void* targets, const float* lse, const float* dloss,
+                                    void* dx, void* dtable, void* workspace, cudaStream_t st);
+
 // ---- CUDA cores (xent_portable.cu) ---------------------------------------------
-// Forward: part[slice][row] = (maximum, sum) over the slice's logits, zt[row]
-// the target's logit where the row has a target.
 int xent_portable_slices(const TableProblem& p);
 cudaError_t launch_xent_portable(const TableProblem& p, const void* x, const void* table,
                                  const void* targets, float2* part, float* zt, cudaStream_t st);

@@ -74,7 +74,7 @@ __device__ __forceinline__ void tile_product(const Operand<TA>& A, const Operand
 template <typename T, typename I>
 __global__ void __launch_bounds__(kThreads)
 xent_fwd_kernel(const Operand<T> x, const Operand<T> w, const I* __restrict__ targets,
-                float2* __restrict__ part, float* __restrict__ zt, int slice, float scale) {
+                float2* __restrict__ part, float* __restrict__ zt, int slice, float scale2) {
   __shared__ Tiles s;
   wait_prior_grid();
   const int m0 = blockIdx.x * kT, tx = threadIdx.x % 16, ty = threadIdx.x / 16;
@@ -97,7 +97,7 @@ xent_fwd_kernel(const Operand<T> x, const Operand<T> w, const I* __restrict__ ta
       for (int j = 0; j < 4; ++j) {
         const int v = n0 + 4 * tx + j;
         if (v >= v1) continue;
-        const float z = acc[i][j] * scale;
+        const float z = acc[i][j] * scale2;
         if (v == t[i]) zt[m0 + 4 * ty + i] = z;
         lse_add(m[i], sum[i], z, 1.f);
       }
@@ -197,7 +197,7 @@ cudaError_t fwd_t(const TableProblem& p, const void* x, const void* table, const
   const Operand<T> W{static_cast<const T*>(table), (size_t)p.d, 1, p.vocab, p.d};
   cudaError_t e =
       launch_dependent(xent_fwd_kernel<T, I>, dim3(tiles_of(p.rows), slices), dim3(kThreads), 0,
-                       st, X, W, static_cast<const I*>(targets), part, zt, slice, p.scale);
+                       st, X, W, static_cast<const I*>(targets), part, zt, slice, p.scale * kLog2e);
   if (e == cudaSuccess) note_launch();
   return e;
 }

@@ -1,0 +1,827 @@
+// The cross entropy's products on the 5th-generation tensor cores, and the
+// parts of it that run in their epilogues (xent_portable.cu has the formulas):
+//   logits   Z = x W^T       -> each row's maximum and sum of exponentials
+//   gradient Z = x W^T       -> g = scale dloss (exp(Z - lse) - [v = t])
+//   dx = g W,  dW = g^T x    -> stored, or added to the sum of earlier pieces
+// One kernel does all of them: a persistent GEMM of CTA pairs (cta_group::2).
+// A pair computes 256 x `width` (<= 256) tiles of D = A B^T; each CTA stages
+// its 128 rows of A and its half of B's columns, 64 of K at a time, and holds
+// its 128 rows of D in tensor memory, twice, so that the next tile's products
+// run while the epilogue reads the last one.  Per CTA:
+//   warp 0      TMA loads into a ring of kStages stages;
+//   warp 1      allocates tensor memory; in CTA 0 one thread issues the MMAs;
+//   warps 2..9  epilogue, two warps per quadrant of TMEM lanes, which share a
+//               tile's 64-column groups between them.
+// Operands stand K-major (x and W for the logits, g for dx) or MN-major (W for
+// dx; g and x for dW), so that no transposed copy is made.
+//
+// float32 operands are taken apart into three bfloat16 values each (24 bits
+// of significand), and the six products of planes that matter are summed
+// in the same float32 accumulator, small ones first: the three left out are
+// below 2^-24 of the largest.
+#include <algorithm>
+
+#include "common.cuh"
+#include "internal.h"
+#include "sm100.cuh"
+#include "vec16.cuh"
+#include "xent.cuh"
+
+namespace lsh {
+namespace {
+
+using namespace sm100;
+
+constexpr int kTileM = 256;   // rows of a pair's tile, 128 per CTA
+constexpr int kTileN = 256;   // most columns of a tile
+constexpr int kBlockK = 64;   // one 128-byte swizzled row of bf16
+constexpr int kStages = 6;
+constexpr int kOperand = 128 * kBlockK * 2;  // bytes of one CTA's A or B in a stage
+constexpr int kEpiWarps = 8;
+constexpr int kThreads = (2 + kEpiWarps) * 32;
+constexpr int kStaging = 32 * 128;  // bytes per epilogue warp: 32 rows of 128 bytes
+constexpr int kBars = 2 * kStages + 5;
+constexpr int kSmem = 1024 + kStages * 2 * kOperand + kEpiWarps * kStaging + kBars * 8 + 16;
+static_assert(kSmem <= 227 * 1024, "shared memory");
+
+enum class Epi { kLse, kGrad, kStore, kAdd };
+
+struct Gemm {
+  int rows, cols;         // of D
+  int m_tiles, n_tiles, width, last_width;
+  int run, slices;        // n tiles of one work item, items per m tile
+  int splits, kb_split;   // K in `splits` parts of kb_split blocks
+  int kb;                 // K blocks of 64
+  int products;           // 1, or the 6 of three planes each
+  int group;              // m tiles that are walked together
+  int items;
+  bool a_mn, b_mn;
+};
+
+struct Params {
+  Gemm g;
+  unsigned int* err;
+  // logits and gradient
+  const void* targets;
+  float scale;
+  float2* part;           // [slices * 2][rows]
+  float* zt;              // [rows]
+  const float* lse;
+  const float* dloss;
+  int v0, vocab;          // the piece's first word
+};
+
+struct Item {
+  int m, n0, n1, k0, k1, split;
+};
+
+__device__ __forceinline__ Item decode(const Gemm& g, int item) {
+  Item it;
+  const int per = g.m_tiles * g.slices;
+  it.split = item / per;
+  const int r = item - it.split * per;
+  const int grp = r / (g.group * g.slices);
+  const int size = min(g.group, g.m_tiles - grp * g.group);
+  const int q = r - grp * g.group * g.slices;
+  it.m = grp * g.group + q % size;
+  it.n0 = q / size * g.run;
+  it.n1 = min(g.n_tiles, it.n0 + g.run);
+  it.k0 = it.split * g.kb_split;
+  it.k1 = min(g.kb, it.k0 + g.kb_split);
+  return it;
+}
+
+// Planes of A and B in product i of a float32 product, two bits each, smallest
+// products first: (0,2) (2,0) (1,1) (0,1) (1,0) (0,0).
+__device__ __forceinline__ int plane_a(int products, int i) {
+  return products == 1 ? 0 : (0x0118 >> (2 * i)) & 3;
+}
+__device__ __forceinline__ int plane_b(int products, int i) {
+  return products == 1 ? 0 : (0x0052 >> (2 * i)) & 3;
+}
+
+// MN-major operand, 128-byte swizzle: rows of 64 elements of M or N (one row
+// per k), groups of 8 k 1024 bytes apart, the next 64 elements 8192 bytes on.
+__device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(8192 >> 4) << 16) |
+         ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// T: type of D (or g) in memory; planes: 1 or 3 bf16 planes of g.
+template <Epi kEpi, typename T, typename I>
+__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
+xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
+               const __grid_constant__ CUtensorMap omap, const Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t* a_smem = smem;
+  uint8_t* b_smem = smem + kStages * kOperand;
+  uint8_t* staging = smem + 2 * kStages * kOperand;
+  uint64_t* full = reinterpret_cast<uint64_t*>(staging + kEpiWarps * kStaging);  // CTA 0's
+  uint64_t* empty = full + kStages;
+  uint64_t* t_full = empty + kStages;   // [2]
+  uint64_t* t_empty = t_full + 2;       // [2], CTA 0's
+  uint64_t* done = t_empty + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const Gemm& g = p.g;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int rank = (int)cluster_ctarank();
+  const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&t_full[b], 1);
+      mbar_init(&t_empty[b], 2 * kEpiWarps);
+    }
+    mbar_init(done, 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc_pair(tmem_slot, 512);
+  tc_fence_before_sync();
+  cluster_sync();
+  tc_fence_after_sync();
+  const uint32_t tmem = *tmem_slot;
+  wait_prior_grid();
+
+  if (warp == 0) {
+    // -------------------------------------------------------------- loads
+    if (lane == 0) {
+      tma_prefetch_desc(&amap);
+      tma_prefetch_desc(&bmap);
+      const int b_boxes = g.b_mn ? (g.width / 2 + 63) / 64 : 1;
+      const uint32_t b_bytes = g.b_mn ? b_boxes * 8192 : g.width / 2 * 128;
+      const uint32_t bytes = 2 * (kOperand + b_bytes);  // of both CTAs
+      int n_loads = 0;
+      bool ok = true;
+      for (int item = pair; ok && item < g.items; item += pairs) {
+        const Item it = decode(g, item);
+        const int m0 = it.m * kTileM + rank * 128;
+        for (int n = it.n0; ok && n < it.n1; ++n) {
+          const int nw = n == g.n_tiles - 1 ? g.last_width : g.width;
+          const int c0 = n * g.width + rank * (nw / 2);
+          for (int pr = 0; ok && pr < g.products; ++pr) {
+            const int za = plane_a(g.products, pr), zb = plane_b(g.products, pr);
+            for (int kb = it.k0; kb < it.k1; ++kb, ++n_loads) {
+              const int s = n_loads % kStages;
+              if (!mbar_wait_cluster(&empty[s], ((n_loads / kStages) & 1) ^ 1, abort_flag)) {
+                ok = false;
+                break;
+              }
+              if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
+              const uint32_t bar = cluster_addr(&full[s], 0);
+              uint8_t* a = a_smem + s * kOperand;
+              uint8_t* b = b_smem + s * kOperand;
+              const int k = kb * kBlockK;
+              if (g.a_mn) {
+                tma_load_3d_pair(a, &amap, bar, m0, k, za);
+                tma_load_3d_pair(a + 8192, &amap, bar, m0 + 64, k, za);
+              } else {
+                tma_load_3d_pair(a, &amap, bar, k, m0, za);
+              }
+              if (g.b_mn) {
+                for (int j = 0; j < b_boxes; ++j)
+                  tma_load_3d_pair(b + j * 8192, &bmap, bar, c0 + 64 * j, k, zb);
+              } else {
+                tma_load_3d_pair(b, &bmap, bar, k, c0, zb);
+              }
+            }
+          }
+        }
+      }
+      if (!ok) {
+        atomicOr(p.err, kErrWaitProducer);
+        *abort_flag = 1;
+      }
+      // The last loads must land before either CTA may exit (CTA 1 waits for
+      // CTA 0 at the end).
+      if (rank == 0)
+        for (int l = n_loads > kStages ? n_loads - kStages : 0; l < n_loads; ++l) {
+          const unsigned long long t0 = globaltimer();
+          while (!mbar_try_wait(&full[l % kStages], (l / kStages) & 1)) {
+            if (globaltimer() - t0 > kWaitLimitNs) { atomicOr(p.err, kErrWaitDrain); break; }
+          }
+        }
+    }
+  } else if (warp == 1) {
+    // -------------------------------------------------------------- MMAs
+    if (rank == 0 && lane == 0) {
+      const uint32_t major = (g.a_mn ? 1u << 15 : 0u) | (g.b_mn ? 1u << 16 : 0u);
+      const uint32_t a_step = g.a_mn ? 2048 : 32, b_step = g.b_mn ? 2048 : 32;  // 16 of K
+      int n_loads = 0, tile = 0;
+      bool ok = true, issued = false;
+      for (int item = pair; ok && item < g.items; item += pairs) {
+        const Item it = decode(g, item);
+        const int blocks = (it.k1 - it.k0) * g.products;
+        for (int n = it.n0; ok && n < it.n1; ++n, ++tile) {
+          const int nw = n == g.n_tiles - 1 ? g.last_width : g.width;
+          const uint32_t idesc = idesc_bf16_f32(kTileM, nw) | major;
+          const int buf = tile & 1;
+          const uint32_t d = tmem + buf * kTileN;
+          if (!mbar_wait_cluster(&t_empty[buf], ((tile >> 1) & 1) ^ 1, abort_flag)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after_sync();
+          for (int kb = 0; kb < blocks; ++kb, ++n_loads) {
+            const int s = n_loads % kStages;
+            if (!mbar_wait_cluster(&full[s], (n_loads / kStages) & 1, abort_flag)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after_sync();
+            const uint32_t a = smem_u32(a_smem + s * kOperand);
+            const uint32_t b = smem_u32(b_smem + s * kOperand);
+#pragma unroll
+            for (int k = 0; k < kBlockK / 16; ++k)
+              mma_bf16_ss_pair(d, g.a_mn ? sdesc_mn(a + k * a_step) : sdesc_kmajor_sw128(a + k * a_step),
+                               g.b_mn ? sdesc_mn(b + k * b_step) : sdesc_kmajor_sw128(b + k * b_step),
+                               idesc, kb > 0 || k > 0);
+            issued = true;
+            mma_commit_pair(&empty[s]);
+          }
+          if (ok) mma_commit_pair(&t_full[buf]);
+        }
+      }
+      if (!ok) {
+        atomicOr(p.err, kErrWaitMma);
+        *abort_flag = 1;
+      }
+      if (issued) {  // every MMA finishes before tensor memory is released
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                smem_u32(done))
+            : "memory");
+        const unsigned long long t0 = globaltimer();
+        while (!mbar_try_wait(done, 0)) {
+          if (globaltimer() - t0 > kWaitLimitNs) { atomicOr(p.err, kErrWaitDrain); break; }
+        }
+      }
+    }
+  } else {
+    // -------------------------------------------------------------- epilogue
+    const int ew = warp - 2, quad = warp & 3, half = ew >> 2;
+    const uint32_t lane_addr = tmem + ((uint32_t)(quad * 32) << 16);
+    uint8_t* mine = staging + ew * kStaging;
+    const I* targets = static_cast<const I*>(p.targets);
+    const float c = p.scale * kLog2e;
+    int tile = 0;
+    bool ok = true;
+    // 16 bytes of this lane's row of the staging tile
+    auto put = [&](int chunk, uint4 v) {
+      *reinterpret_cast<uint4*>(mine + lane * 128 + ((chunk ^ (lane & 7)) << 4)) = v;
+    };
+    auto stage_free = [&] {
+      if (lane == 0) bulk_wait_read();
+      __syncwarp();
+    };
+    auto send = [&](int x, int y, int z) {
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0 && x < g.cols && y < g.rows) {
+        if constexpr (kEpi == Epi::kAdd) tma_add_3d(&omap, mine, x, y, z);
+        else tma_store_3d(&omap, mine, x, y, z);
+        bulk_commit();
+      }
+    };
+    for (int item = pair; ok && item < g.items; item += pairs) {
+      const Item it = decode(g, item);
+      const int row0 = it.m * kTileM + rank * 128 + quad * 32, row = row0 + lane;
+      int target = -1;
+      float run_m = -INFINITY, run_s = 0.f, up = 0.f, lse2 = 0.f;
+      if constexpr (kEpi == Epi::kLse || kEpi == Epi::kGrad) {
+        if (row < g.rows) {
+          target = target_of(targets, row, p.vocab);
+          if constexpr (kEpi == Epi::kGrad) {
+            up = target >= 0 ? p.dloss[row] * p.scale : 0.f;
+            lse2 = p.lse[row] * kLog2e;
+          }
+        }
+      }
+      for (int n = it.n0; ok && n < it.n1; ++n, ++tile) {
+        const int buf = tile & 1;
+        if (!mbar_wait_cluster(&t_full[buf], (tile >> 1) & 1, abort_flag)) { ok = false; break; }
+        __syncwarp();
+        tc_fence_after_sync();
+        const int nw = n == g.n_tiles - 1 ? g.last_width : g.width;
+        const int groups = (nw + 63) / 64;
+        const int col0 = n * g.width;
+        for (int q = half; q < groups; q += 2) {
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t u[32];
+            const int col = q * 64 + h * 32;      // in the tile
+            const int cc = col0 + col;            // in D
+            tmem_ld_32x32b_x32(lane_addr + (uint32_t)(buf * kTileN + col), u);
+            tmem_ld_wait(u);
+            if constexpr (kEpi == Epi::kLse) {
+              const int there = g.cols - cc;  // columns of the chunk that exist
+              if (there <= 0) continue;
+              float z[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) z[i] = __uint_as_float(u[i]) * c;
+              if (there < 32) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) z[i] = i < there ? z[i] : -INFINITY;
+              }
+              if ((unsigned)(target - cc) < 32u) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (target - cc == i) p.zt[row] = z[i];
+              }
+              float top = run_m;
+#pragma unroll
+              for (int i = 0; i < 32; ++i) top = fmaxf(top, z[i]);
+              const float ref = top == -INFINITY ? 0.f : top;
+              float a[4] = {run_s * ex2(run_m - ref), 0.f, 0.f, 0.f};
+#pragma unroll
+              for (int i = 0; i < 32; ++i) a[i & 3] += ex2(z[i] - ref);
+              run_s = (a[0] + a[1]) + (a[2] + a[3]);
+              run_m = top;
+            } else if constexpr (kEpi == Epi::kGrad) {
+              float z[32];
+#pragma unroll
+              for (int i = 0; i < 32; ++i) z[i] = ex2(fmaf(__uint_as_float(u[i]), c, -lse2));
+              const int at = target - p.v0 - cc;
+              if ((unsigned)at < 32u) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) z[i] -= at == i ? 1.f : 0.f;
+              }
+#pragma unroll
+              for (int i = 0; i < 32; ++i) z[i] = target >= 0 ? up * z[i] : 0.f;
+              constexpr bool kSplit = sizeof(T) == 4;
+              if (!kSplit) {
+                if (h == 0) stage_free();
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                  uint4 v;
+                  __nv_bfloat162* b2 = reinterpret_cast<__nv_bfloat162*>(&v);
+#pragma unroll
+                  for (int i = 0; i < 4; ++i)
+                    b2[i] = __floats2bfloat162_rn(z[8 * j + 2 * i], z[8 * j + 2 * i + 1]);
+                  put(4 * h + j, v);
+                }
+                if (h == 1) send(cc - 32, row0, 0);
+              } else {
+                // three planes, 32 columns each; a box of 64 would need both
+                // halves of the group at once
+#pragma unroll
+                for (int pl = 0; pl < 3; ++pl) {
+                  stage_free();
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) {
+                    uint4 v;
+                    __nv_bfloat162* b2 = reinterpret_cast<__nv_bfloat162*>(&v);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                      float& z0 = z[8 * j + 2 * i];
+                      float& z1 = z[8 * j + 2 * i + 1];
+                      b2[i] = __floats2bfloat162_rn(z0, z1);
+                      const float2 f = __bfloat1622float2(b2[i]);
+                      z0 -= f.x;
+                      z1 -= f.y;
+                    }
+                    *reinterpret_cast<uint4*>(mine + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) = v;
+                  }
+                  send(cc, row0, pl);
+                }
+              }
+            } else if constexpr (sizeof(T) == 4) {
+              stage_free();
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                put(j, make_uint4(u[4 * j], u[4 * j + 1], u[4 * j + 2], u[4 * j + 3]));
+              send(cc, row0, it.split);
+            } else {
+              if (h == 0) stage_free();
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                uint4 v;
+                __nv_bfloat162* b2 = reinterpret_cast<__nv_bfloat162*>(&v);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                  b2[i] = __floats2bfloat162_rn(__uint_as_float(u[8 * j + 2 * i]),
+                                                __uint_as_float(u[8 * j + 2 * i + 1]));
+                put(4 * h + j, v);
+              }
+              if (h == 1) send(cc - 32, row0, it.split);
+            }
+          }
+        }
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(cluster_addr(&t_empty[buf], 0));
+      }
+      if constexpr (kEpi == Epi::kLse) {
+        if (ok && row < g.rows)
+          p.part[(size_t)(it.n0 / g.run * 2 + half) * g.rows + row] = make_float2(run_m, run_s);
+      }
+    }
+    if constexpr (kEpi != Epi::kLse) {
+      if (lane == 0) bulk_wait();
+    }
+    if (!ok) {
+      atomicOr(p.err, kErrWaitEpilogue);
+      *abort_flag = 1;
+    }
+  }
+  __syncwarp();
+  tc_fence_before_sync();
+  cluster_sync();
+  tc_fence_after_sync();
+  if (warp == 1) tmem_dealloc_pair(tmem, 512);
+}
+
+// ---------------------------------------------------------------- preparation
+// planes[3][rows][d]: three bfloat16 values whose sum is the float32 value to
+// 24 bits; zeros in rows without a target when `targets` is given.
+template <typename I>
+__global__ void __launch_bounds__(256)
+xent_planes_kernel(const float* __restrict__ src, const I* __restrict__ targets,
+                   __nv_bfloat16* __restrict__ planes, long long pieces, int per_row, int vocab) {
+  wait_prior_grid();
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (i >= pieces) return;
+  float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+  if (!targets || target_of(targets, i / per_row, vocab) >= 0) {
+    Vec16<float>::load(src + i * 8, f);
+    Vec16<float>::load(src + i * 8 + 4, f + 4);
+  }
+#pragma unroll
+  for (int pl = 0; pl < 3; ++pl) {
+    Vec16<__nv_bfloat16>::store(planes + ((size_t)pl * pieces + i) * 8, f);
+#pragma unroll
+    for (int t = 0; t < 8; ++t) f[t] -= __bfloat162float(__float2bfloat16_rn(f[t]));
+  }
+}
+
+// out = the sum of the planes, in their order.
+template <typename T>
+__global__ void __launch_bounds__(256)
+xent_sum_kernel(const float* __restrict__ sums, T* __restrict__ out, long long pieces, int planes) {
+  wait_prior_grid();
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (i >= pieces) return;
+  float a[8];
+#pragma unroll
+  for (int t = 0; t < 8; ++t) a[t] = 0.f;
+  for (int s = 0; s < planes; ++s) {
+    float f[8];
+    Vec16<float>::load(sums + ((size_t)s * pieces + i) * 8, f);
+    Vec16<float>::load(sums + ((size_t)s * pieces + i) * 8 + 4, f + 4);
+#pragma unroll
+    for (int t = 0; t < 8; ++t) a[t] += f[t];
+  }
+#pragma unroll
+  for (int t = 0; t < 8; t += Vec16<T>::N) Vec16<T>::store(out + i * 8 + t, a + t);
+}
+
+// ---------------------------------------------------------------- host side
+size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
+int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
+int pairs_of_device() { return std::max(1, sm_count() / 2); }
+
+// Columns of D cut into tiles of `width`, a multiple of 64: the fewest that
+// 256 allows, or more of them while pairs would stand idle.
+void set_columns(Gemm* g, int cols) {
+  g->cols = cols;
+  const int fewest = ceil_div(cols, kTileN);
+  const int idle = ceil_div(pairs_of_device(), g->m_tiles);
+  const int n = std::max(fewest, std::min(ceil_div(cols, 64), idle));
+  g->width = ceil_div(ceil_div(cols, n), 64) * 64;
+  g->n_tiles = ceil_div(cols, g->width);
+  g->last_width = ceil_div(cols - (g->n_tiles - 1) * g->width, 32) * 32;  // N of a pair's MMA
+}
+
+Gemm make_gemm(long long rows, int cols, int k, bool f32, bool a_mn, bool b_mn) {
+  Gemm g = {};
+  g.rows = (int)rows;
+  g.m_tiles = ceil_div(rows, kTileM);
+  set_columns(&g, cols);
+  g.run = 1;
+  g.slices = g.n_tiles;
+  g.kb = ceil_div(k, kBlockK);
+  g.splits = 1;
+  g.kb_split = g.kb;
+  g.products = f32 ? 6 : 1;
+  g.group = 16;
+  g.items = g.m_tiles * g.slices;
+  g.a_mn = a_mn;
+  g.b_mn = b_mn;
+  return g;
+}
+
+// Logits: a work item is a run of n tiles of one m tile, with one pair of
+// partial results per row.  The longest run that costs at most 2% more time
+// than the best one.
+Gemm logits_gemm(const TableProblem& p) {
+  Gemm g = make_gemm(p.rows, p.vocab, p.d, !p.bf16, false, false);
+  const int pairs = pairs_of_device();
+  auto span = [&](int run) {
+    return (long long)ceil_div((long long)g.m_tiles * ceil_div(g.n_tiles, run), pairs) * run;
+  };
+  long long best = span(1);
+  const int most = std::min(g.n_tiles, 256);
+  for (int run = 2; run <= most; ++run) best = std::min(best, span(run));
+  for (int run = 1; run <= most; ++run)
+    if (span(run) * 50 <= best * 51) g.run = run;
+  g.slices = ceil_div(g.n_tiles, g.run);
+  g.items = g.m_tiles * g.slices;
+  g.group = 64;
+  return g;
+}
+
+// Cut K where whole tiles would leave pairs idle: cost in blocks of K, with
+// kTileCost blocks to fill and empty the pipeline per tile and the time of the
+// partial sums' traffic (a block takes about 0.35 us, HBM moves about 2 MB in that).
+void set_splits(Gemm* g) {
+  constexpr int kTileCost = 6;
+  const int pairs = pairs_of_device(), tiles = g->m_tiles * g->n_tiles;
+  const double plane = (double)g->rows * g->cols * 4 / 2e6;
+  double best = 0;
+  for (int s = 1; s <= 8 && s <= g->kb; ++s) {
+    const int kb = ceil_div(g->kb, s);
+    if (ceil_div(g->kb, kb) != s) continue;
+    const double cost = (double)ceil_div((long long)tiles * s, pairs) * (kb * g->products + kTileCost) +
+                        (s > 1 ? 2 * s * plane : 0.0);
+    if (s == 1 || cost < best) {
+      best = cost;
+      g->splits = s;
+      g->kb_split = kb;
+    }
+  }
+  g->items = g->m_tiles * g->n_tiles * g->splits;
+}
+
+// The backward's pieces: g of `words` columns (a multiple of 256) within
+// kGradBytes.  Among those, the count whose pieces take the fewest waves of
+// dW tiles, then the largest.
+constexpr size_t kGradBytes = 512u << 20;
+struct Backward {
+  int words, pieces;
+  size_t ld;             // columns of g
+  bool sum_dx, sum_dw;   // float32 sums outside the results
+  int dx_splits, dw_splits;
+  size_t clean, w_planes, g, dx_sums, dw_sums, total;
+};
+
+Gemm dx_gemm(const TableProblem& p, int words) {
+  Gemm g = make_gemm(p.rows, p.d, words, !p.bf16, false, true);
+  set_splits(&g);
+  return g;
+}
+
+Gemm dw_gemm(const TableProblem& p, int words) {
+  Gemm g = make_gemm(words, p.d, (int)p.rows, !p.bf16, true, true);
+  set_splits(&g);
+  return g;
+}
+
+Backward plan_backward(const TableProblem& p) {
+  Backward b;
+  const int planes = p.bf16 ? 1 : 3, pairs = pairs_of_device();
+  const int all = ceil_div(p.vocab, kTileM), nt = ceil_div(p.d, kTileN);
+  const size_t per_tile = (size_t)planes * p.rows * kTileM * 2;
+  const int most = (int)std::min<size_t>(all, std::max<size_t>(1, kGradBytes / per_tile));
+  int tiles = most;
+  if (most < all) {
+    long long best = -1;
+    for (int t = most; t >= 1 && t >= most / 2; --t) {
+      const int rest = all % t;
+      const long long waves = (long long)(all / t) * ceil_div((long long)t * nt, pairs) +
+                              ceil_div((long long)rest * nt, pairs);
+      if (best < 0 || waves < best) { best = waves; tiles = t; }
+    }
+  }
+  b.words = tiles * kTileM;
+  b.pieces = ceil_div(all, tiles);
+  b.ld = (size_t)b.words;
+  // splits are fixed by the full pieces; the last one, if shorter, keeps them
+  b.dx_splits = dx_gemm(p, b.pieces == 1 ? p.vocab : b.words).splits;
+  b.dw_splits = dw_gemm(p, b.pieces == 1 ? p.vocab : b.words).splits;
+  // with float32 results and no split K the result itself is the sum
+  b.sum_dx = b.dx_splits > 1 || (b.pieces > 1 && p.bf16);
+  b.sum_dw = b.dw_splits > 1;
+  const size_t nd = (size_t)p.rows * p.d, vd = (size_t)b.words * p.d;
+  size_t off = 0;
+  b.clean = off;    off += align256(nd * 2 * planes);
+  b.w_planes = off; off += p.bf16 ? 0 : align256((size_t)p.vocab * p.d * 6);
+  b.g = off;        off += align256((size_t)planes * p.rows * b.ld * 2);
+  b.dx_sums = off;  off += b.sum_dx ? align256(nd * 4 * b.dx_splits) : 0;
+  b.dw_sums = off;  off += b.sum_dw ? align256(vd * 4 * b.dw_splits) : 0;
+  b.total = off;
+  return b;
+}
+
+// A tensor of `planes` matrices [rows][ld] of which `cols` columns count.
+bool encode(CUtensorMap* map, const void* base, bool f32, long long cols, long long rows,
+            long long planes, size_t ld, long long plane_rows, int box_x, int box_y,
+            CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
+  const size_t elem = f32 ? 4 : 2;
+  const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)planes};
+  const cuuint64_t strides[2] = {(cuuint64_t)(ld * elem), (cuuint64_t)(ld * elem * plane_rows)};
+  const cuuint32_t box[3] = {(cuuint32_t)box_x, (cuuint32_t)box_y, 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return tensor_map_encoder()(map, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32
+                                       : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+                              3, const_cast<void*>(base), dims, strides, box, estr,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <Epi kEpi, typename T, typename I>
+cudaError_t launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o,
+                   const Params& p, cudaStream_t st) {
+  auto kernel = xent_tc_kernel<kEpi, T, I>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e) return e;
+  const int pairs = std::min(pairs_of_device(), p.g.items);
+  e = launch_dependent(kernel, dim3(2 * pairs), dim3(kThreads), (size_t)kSmem, st, a, b, o, p);
+  if (e == cudaSuccess) note_launch();
+  return e;
+}
+
+template <Epi kEpi, typename T>
+cudaError_t launch_i(bool idx64, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o,
+                     const Params& p, cudaStream_t st) {
+  return idx64 ? launch<kEpi, T, int64_t>(a, b, o, p, st) : launch<kEpi, T, int32_t>(a, b, o, p, st);
+}
+
+cudaError_t launch_planes(const TableProblem& p, const void* src, long long rows,
+                          const void* targets, void* planes, cudaStream_t st) {
+  const long long pieces = rows * (p.d / 8);
+  const dim3 grid((unsigned)((pieces + 255) / 256)), block(256);
+  __nv_bfloat16* to = static_cast<__nv_bfloat16*>(planes);
+  const float* from = static_cast<const float*>(src);
+  cudaError_t e =
+      p.idx64 ? launch_dependent(xent_planes_kernel<int64_t>, grid, block, 0, st, from,
+                                 static_cast<const int64_t*>(targets), to, pieces, p.d / 8, p.vocab)
+              : launch_dependent(xent_planes_kernel<int32_t>, grid, block, 0, st, from,
+                                 static_cast<const int32_t*>(targets), to, pieces, p.d / 8, p.vocab);
+  if (e == cudaSuccess) note_launch();
+  return e;
+}
+
+cudaError_t launch_sum(bool bf16, const float* sums, void* out, long long values, int planes,
+                       cudaStream_t st) {
+  const long long pieces = values / 8;
+  const dim3 grid((unsigned)((pieces + 255) / 256)), block(256);
+  cudaError_t e = bf16 ? launch_dependent(xent_sum_kernel<__nv_bfloat16>, grid, block, 0, st, sums,
+                                          static_cast<__nv_bfloat16*>(out), pieces, planes)
+                       : launch_dependent(xent_sum_kernel<float>, grid, block, 0, st, sums,
+                                          static_cast<float*>(out), pieces, planes);
+  if (e == cudaSuccess) note_launch();
+  return e;
+}
+
+// Product into rows [0, g.rows) of out: straight into the result (splits == 1)
+// or into g.splits planes of float32 sums; `add` to what is there.
+cudaError_t launch_product(const Gemm& g, const CUtensorMap& a, const CUtensorMap& b, void* out,
+                           bool f32, int d, long long plane_rows, bool add, unsigned int* err,
+                           cudaStream_t st) {
+  CUtensorMap o;
+  if (!encode(&o, out, f32, d, g.rows, g.splits, d, plane_rows, f32 ? 32 : 64, 32))
+    return cudaErrorInvalidValue;
+  Params p = {};
+  p.g = g;
+  p.err = err;
+  if (!f32) return launch<Epi::kStore, __nv_bfloat16, int32_t>(a, b, o, p, st);
+  return add ? launch<Epi::kAdd, float, int32_t>(a, b, o, p, st)
+             : launch<Epi::kStore, float, int32_t>(a, b, o, p, st);
+}
+
+}  // namespace
+
+bool xent_tc_supported(const TableProblem& p) {
+  // (the limit keeps the count of tiles within 32 bits)
+  return !p.portable && tensor_map_encoder() != nullptr && p.rows <= (1 << 24);
+}
+
+int xent_tc_slices(const TableProblem& p) { return 2 * logits_gemm(p).slices; }
+
+size_t xent_tc_bytes(const TableProblem& p) {
+  return p.bf16 ? 0 : align256((size_t)p.rows * p.d * 6) + align256((size_t)p.vocab * p.d * 6);
+}
+
+cudaError_t launch_xent_tc(const TableProblem& p, const void* x, const void* table,
+                           const void* targets, float2* part, float* zt, void* scratch,
+                           cudaStream_t st) {
+  cudaError_t e;
+  const int planes = p.bf16 ? 1 : 3;
+  if (!p.bf16) {
+    void* xp = scratch;
+    void* wp = static_cast<char*>(scratch) + align256((size_t)p.rows * p.d * 6);
+    if ((e = launch_planes(p, x, p.rows, nullptr, xp, st))) return e;
+    if ((e = launch_planes(p, table, p.vocab, nullptr, wp, st))) return e;
+    x = xp;
+    table = wp;
+  }
+  Params k = {};
+  k.g = logits_gemm(p);
+  k.err = device_error_word();
+  if (!k.err) return cudaErrorUnknown;
+  k.targets = targets;
+  k.scale = p.scale;
+  k.part = part;
+  k.zt = zt;
+  k.vocab = p.vocab;
+  CUtensorMap a, b;
+  if (!encode(&a, x, false, p.d, p.rows, planes, p.d, p.rows, kBlockK, 128) ||
+      !encode(&b, table, false, p.d, p.vocab, planes, p.d, p.vocab, kBlockK, k.g.width / 2))
+    return cudaErrorInvalidValue;
+  return launch_i<Epi::kLse, float>(p.idx64, a, b, a, k, st);
+}
+
+size_t xent_tc_backward_bytes(const TableProblem& p) { return plan_backward(p).total; }
+
+cudaError_t launch_xent_tc_backward(const TableProblem& p, const void* x, const void* table,
+                                    const void* targets, const float* lse, const float* dloss,
+                                    void* dx, void* dtable, void* workspace, cudaStream_t st) {
+  const Backward plan = plan_backward(p);
+  char* ws = static_cast<char*>(workspace);
+  const int planes = p.bf16 ? 1 : 3;
+  const bool f32 = !p.bf16;
+  unsigned int* err = device_error_word();
+  if (!err) return cudaErrorUnknown;
+  cudaError_t e;
+  void* clean = ws + plan.clean;
+  const void* w = table;
+  if (f32) {
+    if ((e = launch_planes(p, x, p.rows, targets, clean, st))) return e;
+    if ((e = launch_planes(p, table, p.vocab, nullptr, ws + plan.w_planes, st))) return e;
+    w = ws + plan.w_planes;
+  } else {
+    if ((e = launch_xent_clean(p, x, targets, clean, st))) return e;
+  }
+  void* gbuf = ws + plan.g;
+  float* dx_sums = reinterpret_cast<float*>(ws + plan.dx_sums);
+  float* dw_sums = reinterpret_cast<float*>(ws + plan.dw_sums);
+  CUtensorMap x_k, x_mn, w_k, w_mn, g_k, g_mn, g_out;
+  if (!encode(&x_k, clean, false, p.d, p.rows, planes, p.d, p.rows, kBlockK, 128) ||
+      !encode(&x_mn, clean, false, p.d, p.rows, planes, p.d, p.rows, 64, kBlockK))
+    return cudaErrorInvalidValue;
+  for (int v0 = 0; v0 < p.vocab; v0 += plan.words) {
+    const int nv = std::min(plan.words, p.vocab - v0);
+    const char* wv = static_cast<const char*>(w) + (size_t)v0 * p.d * 2;
+    // g of the piece
+    Params k = {};
+    k.g = make_gemm(p.rows, nv, p.d, f32, false, false);
+    k.err = err;
+    k.targets = targets;
+    k.scale = p.scale;
+    k.lse = lse;
+    k.dloss = dloss;
+    k.v0 = v0;
+    k.vocab = p.vocab;
+    // (a piece sees its own words only: rows past them read as zeros)
+    if (!encode(&w_k, wv, false, p.d, nv, planes, p.d, p.vocab, kBlockK, k.g.width / 2) ||
+        !encode(&w_mn, wv, false, p.d, nv, planes, p.d, p.vocab, 64, kBlockK) ||
+        !encode(&g_k, gbuf, false, nv, p.rows, planes, plan.ld, p.rows, kBlockK, 128) ||
+        !encode(&g_mn, gbuf, false, nv, p.rows, planes, plan.ld, p.rows, 64, kBlockK) ||
+        !encode(&g_out, gbuf, false, nv, p.rows, planes, plan.ld, p.rows, f32 ? 32 : 64, 32,
+                f32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B))
+      return cudaErrorInvalidValue;
+    e = f32 ? launch_i<Epi::kGrad, float>(p.idx64, x_k, w_k, g_out, k, st)
+            : launch_i<Epi::kGrad, __nv_bfloat16>(p.idx64, x_k, w_k, g_out, k, st);
+    if (e) return e;
+    // dx += g W
+    Gemm gx = make_gemm(p.rows, p.d, nv, f32, false, true);
+    // (a last, shorter piece may have blocks for fewer parts only)
+    gx.kb_split = ceil_div(gx.kb, plan.dx_splits);
+    gx.splits = ceil_div(gx.kb, gx.kb_split);
+    gx.items = gx.m_tiles * gx.n_tiles * gx.splits;
+    void* dx_to = plan.sum_dx ? static_cast<void*>(dx_sums) : dx;
+    if ((e = launch_product(gx, g_k, w_mn, dx_to, f32 || plan.sum_dx, p.d, p.rows, v0 > 0, err, st)))
+      return e;
+    // dW = g^T x
+    Gemm gw = make_gemm(nv, p.d, (int)p.rows, f32, true, true);
+    gw.splits = plan.dw_splits;
+    gw.kb_split = ceil_div(gw.kb, gw.splits);
+    gw.items = gw.m_tiles * gw.n_tiles * gw.splits;
+    char* dw_at = static_cast<char*>(dtable) + (size_t)v0 * p.d * p.elem();
+    void* dw_to = plan.sum_dw ? static_cast<void*>(dw_sums) : dw_at;
+    if ((e = launch_product(gw, g_mn, x_mn, dw_to, f32 || plan.sum_dw, p.d, nv, false, err, st)))
+      return e;
+    if (plan.sum_dw &&
+        (e = launch_sum(p.bf16, dw_sums, dw_at, (long long)nv * p.d, gw.splits, st)))
+      return e;
+  }
+  if (plan.sum_dx)
+    return launch_sum(p.bf16, dx_sums, dx, p.rows * p.d, plan.dx_splits, st);
+  return cudaSuccess;
+}
+
+}  // namespace lsh

@@ -155,6 +155,19 @@ def test_xent(n, vocab, d, dtype, index, scale, holes, portable):
     assert torch.equal(again[0], dx) and torch.equal(again[1], dw)
 
 
+@pytest.mark.parametrize("n,vocab,d,dtype", [(20011, 14001, 24, BF16), (9001, 10007, 40, F32)])
+def test_xent_backward_in_pieces(n, vocab, d, dtype):
+    # more gradient values than one piece of the vocabulary holds
+    x, table, t, dloss = make_xent(n, vocab, d, dtype, torch.int64, 0.02)
+    lse = lsh.lsh_attn_xent(x, table, t)[1]
+    dx, dw = lsh.lsh_attn_xent_backward(x, table, t, lse, dloss)
+    want_dx, want_dw = R.xent_backward(x, table, t, dloss, 1.0, BF16 if dtype == BF16 else None)
+    R.check("dx", dx, want_dx)
+    R.check("dtable", dw, want_dw)
+    again = lsh.lsh_attn_xent_backward(x, table, t, lse, dloss)
+    assert torch.equal(again[0], dx) and torch.equal(again[1], dw)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_xent_of_no_rows(dtype):
     x, table = torch.empty(0, 16, device=DEV, dtype=dtype), randn(gen(0), 9, 16, dtype=dtype)
