@@ -53,6 +53,7 @@ struct Gemm {
   int splits, kb_split;   // K in `splits` parts of kb_split blocks
   int kb;                 // K blocks of 64
   int products;           // 1, or the 6 of three planes each
+  int chunk;              // K blocks summed in one accumulator
   int group;              // m tiles that are walked together
   int items;
   bool a_mn, b_mn;
@@ -113,8 +114,8 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// T: type of D (or g) in memory; planes: 1 or 3 bf16 planes of g.
-template <Epi kEpi, typename T, typename I>
+// T: type of D in memory; kPlanes: float32 operands in three planes each.
+template <Epi kEpi, typename T, typename I, bool kPlanes>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
                const __grid_constant__ CUtensorMap omap, const Params p) {
@@ -172,9 +173,9 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
         for (int n = it.n0; ok && n < it.n1; ++n) {
           const int nw = n == g.n_tiles - 1 ? g.last_width : g.width;
           const int c0 = n * g.width + rank * (nw / 2);
-          for (int pr = 0; ok && pr < g.products; ++pr) {
-            const int za = plane_a(g.products, pr), zb = plane_b(g.products, pr);
-            for (int kb = it.k0; kb < it.k1; ++kb, ++n_loads) {
+          for (int kc = it.k0; ok && kc < it.k1; kc += g.chunk) {
+            const int len = min(it.k1, kc + g.chunk) - kc;
+            for (int i = 0; i < len * g.products; ++i, ++n_loads) {
               const int s = n_loads % kStages;
               if (!mbar_wait_cluster(&empty[s], ((n_loads / kStages) & 1) ^ 1, abort_flag)) {
                 ok = false;
@@ -184,7 +185,9 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
               const uint32_t bar = cluster_addr(&full[s], 0);
               uint8_t* a = a_smem + s * kOperand;
               uint8_t* b = b_smem + s * kOperand;
-              const int k = kb * kBlockK;
+              const int pr = g.products > 1 ? i / len : 0;
+              const int k = (kc + i - pr * len) * kBlockK;
+              const int za = plane_a(g.products, pr), zb = plane_b(g.products, pr);
               if (g.a_mn) {
                 tma_load_3d_pair(a, &amap, bar, m0, k, za);
                 tma_load_3d_pair(a + 8192, &amap, bar, m0 + 64, k, za);
@@ -224,35 +227,39 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
       bool ok = true, issued = false;
       for (int item = pair; ok && item < g.items; item += pairs) {
         const Item it = decode(g, item);
-        const int blocks = (it.k1 - it.k0) * g.products;
-        for (int n = it.n0; ok && n < it.n1; ++n, ++tile) {
+        for (int n = it.n0; ok && n < it.n1; ++n) {
           const int nw = n == g.n_tiles - 1 ? g.last_width : g.width;
           const uint32_t idesc = idesc_bf16_f32(kTileM, nw) | major;
-          const int buf = tile & 1;
-          const uint32_t d = tmem + buf * kTileN;
-          if (!mbar_wait_cluster(&t_empty[buf], ((tile >> 1) & 1) ^ 1, abort_flag)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after_sync();
-          for (int kb = 0; kb < blocks; ++kb, ++n_loads) {
-            const int s = n_loads % kStages;
-            if (!mbar_wait_cluster(&full[s], (n_loads / kStages) & 1, abort_flag)) {
+          for (int kc = it.k0; ok && kc < it.k1; kc += g.chunk, ++tile) {
+            const int blocks = (min(it.k1, kc + g.chunk) - kc) * g.products;
+            const int buf = tile & 1;
+            const uint32_t d = tmem + buf * kTileN;
+            if (!mbar_wait_cluster(&t_empty[buf], ((tile >> 1) & 1) ^ 1, abort_flag)) {
               ok = false;
               break;
             }
             tc_fence_after_sync();
-            const uint32_t a = smem_u32(a_smem + s * kOperand);
-            const uint32_t b = smem_u32(b_smem + s * kOperand);
+            for (int kb = 0; kb < blocks; ++kb, ++n_loads) {
+              const int s = n_loads % kStages;
+              if (!mbar_wait_cluster(&full[s], (n_loads / kStages) & 1, abort_flag)) {
+                ok = false;
+                break;
+              }
+              tc_fence_after_sync();
+              const uint32_t a = smem_u32(a_smem + s * kOperand);
+              const uint32_t b = smem_u32(b_smem + s * kOperand);
 #pragma unroll
-            for (int k = 0; k < kBlockK / 16; ++k)
-              mma_bf16_ss_pair(d, g.a_mn ? sdesc_mn(a + k * a_step) : sdesc_kmajor_sw128(a + k * a_step),
-                               g.b_mn ? sdesc_mn(b + k * b_step) : sdesc_kmajor_sw128(b + k * b_step),
-                               idesc, kb > 0 || k > 0);
-            issued = true;
-            mma_commit_pair(&empty[s]);
+              for (int k = 0; k < kBlockK / 16; ++k) {
+                const uint32_t ak = a + k * a_step, bk = b + k * b_step;
+                mma_bf16_ss_pair(d, g.a_mn ? sdesc_mn(ak) : sdesc_kmajor_sw128(ak),
+                                 g.b_mn ? sdesc_mn(bk) : sdesc_kmajor_sw128(bk), idesc,
+                                 kb > 0 || k > 0);
+              }
+              issued = true;
+              mma_commit_pair(&empty[s]);
+            }
+            if (ok) mma_commit_pair(&t_full[buf]);
           }
-          if (ok) mma_commit_pair(&t_full[buf]);
         }
       }
       if (!ok) {
@@ -279,22 +286,46 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
     const float c = p.scale * kLog2e;
     int tile = 0;
     bool ok = true;
-    // 16 bytes of this lane's row of the staging tile
-    auto put = [&](int chunk, uint4 v) {
-      *reinterpret_cast<uint4*>(mine + lane * 128 + ((chunk ^ (lane & 7)) << 4)) = v;
-    };
-    auto stage_free = [&] {
+    auto stage_free = [&] {  // the last store has read the staging tile
       if (lane == 0) bulk_wait_read();
       __syncwarp();
     };
-    auto send = [&](int x, int y, int z) {
+    auto send = [&](int x, int y, int plane) {
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0 && x < g.cols && y < g.rows) {
-        if constexpr (kEpi == Epi::kAdd) tma_add_3d(&omap, mine, x, y, z);
-        else tma_store_3d(&omap, mine, x, y, z);
+        if constexpr (kEpi == Epi::kAdd) tma_add_3d(&omap, mine, x, y, plane);
+        else tma_store_3d(&omap, mine, x, y, plane);
         bulk_commit();
       }
+    };
+    // 8 values to 16 bytes of bf16; with `rest` what the rounding left stays in z.
+    auto pack8 = [](float* z, bool rest) {
+      uint4 w;
+      __nv_bfloat162* b2 = reinterpret_cast<__nv_bfloat162*>(&w);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        b2[i] = __floats2bfloat162_rn(z[2 * i], z[2 * i + 1]);
+        if (rest) {
+          const float2 f = __bfloat1622float2(b2[i]);
+          z[2 * i] -= f.x;
+          z[2 * i + 1] -= f.y;
+        }
+      }
+      return w;
+    };
+    // 16-byte piece j of this lane's row of 128 or 64 bytes in the staging
+    // tile, swizzled as its tensor map says.
+    auto put128 = [&](int j, uint4 w) {
+      *reinterpret_cast<uint4*>(mine + lane * 128 + ((j ^ (lane & 7)) << 4)) = w;
+    };
+    auto put64 = [&](int j, uint4 w) {
+      *reinterpret_cast<uint4*>(mine + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) = w;
+    };
+    auto release = [&](int buf) {
+      tc_fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(cluster_addr(&t_empty[buf], 0));
     };
     for (int item = pair; ok && item < g.items; item += pairs) {
       const Item it = decode(g, item);
@@ -310,119 +341,111 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
           }
         }
       }
-      for (int n = it.n0; ok && n < it.n1; ++n, ++tile) {
-        const int buf = tile & 1;
-        if (!mbar_wait_cluster(&t_full[buf], (tile >> 1) & 1, abort_flag)) { ok = false; break; }
-        __syncwarp();
-        tc_fence_after_sync();
-        const int nw = n == g.n_tiles - 1 ? g.last_width : g.width;
-        const int groups = (nw + 63) / 64;
-        const int col0 = n * g.width;
-        for (int q = half; q < groups; q += 2) {
+      // Half h, 32 columns at cc of D, of a 64-column group.
+      auto take = [&](float (&z)[32], int h, int cc) {
+        if constexpr (kEpi == Epi::kLse) {
+          const int there = g.cols - cc;  // columns that exist
+          if (there <= 0) return;
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t u[32];
-            const int col = q * 64 + h * 32;      // in the tile
-            const int cc = col0 + col;            // in D
-            tmem_ld_32x32b_x32(lane_addr + (uint32_t)(buf * kTileN + col), u);
-            tmem_ld_wait(u);
-            if constexpr (kEpi == Epi::kLse) {
-              const int there = g.cols - cc;  // columns of the chunk that exist
-              if (there <= 0) continue;
-              float z[32];
+          for (int i = 0; i < 32; ++i) z[i] = i < there ? z[i] * c : -INFINITY;
+          if ((unsigned)(target - cc) < 32u) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) z[i] = __uint_as_float(u[i]) * c;
-              if (there < 32) {
+            for (int i = 0; i < 32; ++i)
+              if (target - cc == i) p.zt[row] = z[i];
+          }
+          float top = run_m;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) z[i] = i < there ? z[i] : -INFINITY;
-              }
-              if ((unsigned)(target - cc) < 32u) {
+          for (int i = 0; i < 32; ++i) top = fmaxf(top, z[i]);
+          const float ref = top == -INFINITY ? 0.f : top;
+          float a[4] = {run_s * ex2(run_m - ref), 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  if (target - cc == i) p.zt[row] = z[i];
-              }
-              float top = run_m;
+          for (int i = 0; i < 32; ++i) a[i & 3] += ex2(z[i] - ref);
+          run_s = (a[0] + a[1]) + (a[2] + a[3]);
+          run_m = top;
+        } else if constexpr (kEpi == Epi::kGrad) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) top = fmaxf(top, z[i]);
-              const float ref = top == -INFINITY ? 0.f : top;
-              float a[4] = {run_s * ex2(run_m - ref), 0.f, 0.f, 0.f};
+          for (int i = 0; i < 32; ++i) z[i] = ex2(fmaf(z[i], c, -lse2));
+          const int at = target - p.v0 - cc;
+          if ((unsigned)at < 32u) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) a[i & 3] += ex2(z[i] - ref);
-              run_s = (a[0] + a[1]) + (a[2] + a[3]);
-              run_m = top;
-            } else if constexpr (kEpi == Epi::kGrad) {
-              float z[32];
+            for (int i = 0; i < 32; ++i) z[i] -= at == i ? 1.f : 0.f;
+          }
+          // a row without a target takes no part, whatever its logits are
 #pragma unroll
-              for (int i = 0; i < 32; ++i) z[i] = ex2(fmaf(__uint_as_float(u[i]), c, -lse2));
-              const int at = target - p.v0 - cc;
-              if ((unsigned)at < 32u) {
+          for (int i = 0; i < 32; ++i) z[i] = target >= 0 ? up * z[i] : 0.f;
+          if constexpr (kPlanes) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) z[i] -= at == i ? 1.f : 0.f;
-              }
-#pragma unroll
-              for (int i = 0; i < 32; ++i) z[i] = target >= 0 ? up * z[i] : 0.f;
-              constexpr bool kSplit = sizeof(T) == 4;
-              if (!kSplit) {
-                if (h == 0) stage_free();
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                  uint4 v;
-                  __nv_bfloat162* b2 = reinterpret_cast<__nv_bfloat162*>(&v);
-#pragma unroll
-                  for (int i = 0; i < 4; ++i)
-                    b2[i] = __floats2bfloat162_rn(z[8 * j + 2 * i], z[8 * j + 2 * i + 1]);
-                  put(4 * h + j, v);
-                }
-                if (h == 1) send(cc - 32, row0, 0);
-              } else {
-                // three planes, 32 columns each; a box of 64 would need both
-                // halves of the group at once
-#pragma unroll
-                for (int pl = 0; pl < 3; ++pl) {
-                  stage_free();
-#pragma unroll
-                  for (int j = 0; j < 4; ++j) {
-                    uint4 v;
-                    __nv_bfloat162* b2 = reinterpret_cast<__nv_bfloat162*>(&v);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                      float& z0 = z[8 * j + 2 * i];
-                      float& z1 = z[8 * j + 2 * i + 1];
-                      b2[i] = __floats2bfloat162_rn(z0, z1);
-                      const float2 f = __bfloat1622float2(b2[i]);
-                      z0 -= f.x;
-                      z1 -= f.y;
-                    }
-                    *reinterpret_cast<uint4*>(mine + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) = v;
-                  }
-                  send(cc, row0, pl);
-                }
-              }
-            } else if constexpr (sizeof(T) == 4) {
+            for (int pl = 0; pl < 3; ++pl) {
               stage_free();
 #pragma unroll
-              for (int j = 0; j < 8; ++j)
-                put(j, make_uint4(u[4 * j], u[4 * j + 1], u[4 * j + 2], u[4 * j + 3]));
-              send(cc, row0, it.split);
-            } else {
-              if (h == 0) stage_free();
+              for (int j = 0; j < 4; ++j) put64(j, pack8(z + 8 * j, true));
+              send(cc, row0, pl);
+            }
+          } else {
+            if (h == 0) stage_free();
 #pragma unroll
-              for (int j = 0; j < 4; ++j) {
-                uint4 v;
-                __nv_bfloat162* b2 = reinterpret_cast<__nv_bfloat162*>(&v);
+            for (int j = 0; j < 4; ++j) put128(4 * h + j, pack8(z + 8 * j, false));
+            if (h == 1) send(cc - 32, row0, 0);
+          }
+        } else if constexpr (sizeof(T) == 4) {
+          stage_free();
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                  b2[i] = __floats2bfloat162_rn(__uint_as_float(u[8 * j + 2 * i]),
-                                                __uint_as_float(u[8 * j + 2 * i + 1]));
-                put(4 * h + j, v);
+          for (int j = 0; j < 8; ++j)
+            put128(j, make_uint4(__float_as_uint(z[4 * j]), __float_as_uint(z[4 * j + 1]),
+                                 __float_as_uint(z[4 * j + 2]), __float_as_uint(z[4 * j + 3])));
+          send(cc, row0, it.split);
+        } else {
+          if (h == 0) stage_free();
+#pragma unroll
+          for (int j = 0; j < 4; ++j) put128(4 * h + j, pack8(z + 8 * j, false));
+          if (h == 1) send(cc - 32, row0, it.split);
+        }
+      };
+      for (int n = it.n0; ok && n < it.n1; ++n) {
+        const int nw = n == g.n_tiles - 1 ? g.last_width : g.width;
+        const int groups = (nw + 63) / 64, col0 = n * g.width;
+        // One accumulator, or with planes the chunks' accumulators added up
+        // in registers (round to nearest, where the tensor core truncates).
+        float sum[2][2][32];
+        for (int kc = it.k0; ok && kc < it.k1; kc += g.chunk, ++tile) {
+          const int buf = tile & 1;
+          if (!mbar_wait_cluster(&t_full[buf], (tile >> 1) & 1, abort_flag)) { ok = false; break; }
+          __syncwarp();
+          tc_fence_after_sync();
+#pragma unroll kPlanes ? 2 : 1
+          for (int gi = 0; gi < 2; ++gi) {
+            const int q = half + 2 * gi;
+            if (q >= groups) continue;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              uint32_t u[32];
+              const int col = q * 64 + h * 32;
+              tmem_ld_32x32b_x32(lane_addr + (uint32_t)(buf * kTileN + col), u);
+              tmem_ld_wait(u);
+              if constexpr (kPlanes) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  sum[gi][h][i] = __uint_as_float(u[i]) + (kc == it.k0 ? 0.f : sum[gi][h][i]);
+              } else {
+                float z[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) z[i] = __uint_as_float(u[i]);
+                take(z, h, col0 + col);
               }
-              if (h == 1) send(cc - 32, row0, it.split);
             }
           }
+          release(buf);
         }
-        tc_fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(cluster_addr(&t_empty[buf], 0));
+        if constexpr (kPlanes) {
+          if (!ok) break;
+#pragma unroll
+          for (int gi = 0; gi < 2; ++gi) {
+            if (half + 2 * gi >= groups) continue;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              take(sum[gi][h], h, col0 + (half + 2 * gi) * 64 + h * 32);
+          }
+        }
       }
       if constexpr (kEpi == Epi::kLse) {
         if (ok && row < g.rows)
@@ -505,6 +528,16 @@ void set_columns(Gemm* g, int cols) {
   g->last_width = ceil_div(cols - (g->n_tiles - 1) * g->width, 32) * 32;  // N of a pair's MMA
 }
 
+// K blocks per accumulator.  The tensor core truncates when it adds to one, an
+// error that grows with the number of additions (1.1e-5 of dx after 500 of
+// them): float32 operands get a new accumulator after kPlaneChunk blocks, 32
+// additions of the largest products.
+constexpr int kPlaneChunk = 8;
+void set_chunk(Gemm* g) {
+  g->chunk = g->kb_split;
+  if (g->products > 1) g->chunk = ceil_div(g->kb_split, ceil_div(g->kb_split, kPlaneChunk));
+}
+
 Gemm make_gemm(long long rows, int cols, int k, bool f32, bool a_mn, bool b_mn) {
   Gemm g = {};
   g.rows = (int)rows;
@@ -516,6 +549,7 @@ Gemm make_gemm(long long rows, int cols, int k, bool f32, bool a_mn, bool b_mn) 
   g.splits = 1;
   g.kb_split = g.kb;
   g.products = f32 ? 6 : 1;
+  set_chunk(&g);
   g.group = 16;
   g.items = g.m_tiles * g.slices;
   g.a_mn = a_mn;
@@ -563,6 +597,7 @@ void set_splits(Gemm* g) {
     }
   }
   g->items = g->m_tiles * g->n_tiles * g->splits;
+  set_chunk(g);
 }
 
 // The backward's pieces: g of `words` columns (a multiple of 256) within
@@ -642,10 +677,10 @@ bool encode(CUtensorMap* map, const void* base, bool f32, long long cols, long l
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <Epi kEpi, typename T, typename I>
+template <Epi kEpi, typename T, typename I, bool kPlanes>
 cudaError_t launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o,
                    const Params& p, cudaStream_t st) {
-  auto kernel = xent_tc_kernel<kEpi, T, I>;
+  auto kernel = xent_tc_kernel<kEpi, T, I, kPlanes>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e) return e;
   const int pairs = std::min(pairs_of_device(), p.g.items);
@@ -654,10 +689,15 @@ cudaError_t launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap
   return e;
 }
 
-template <Epi kEpi, typename T>
-cudaError_t launch_i(bool idx64, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o,
-                     const Params& p, cudaStream_t st) {
-  return idx64 ? launch<kEpi, T, int64_t>(a, b, o, p, st) : launch<kEpi, T, int32_t>(a, b, o, p, st);
+// Logits or gradient of rows whose targets are int64 or int32.
+template <Epi kEpi>
+cudaError_t launch_logits(bool idx64, const CUtensorMap& a, const CUtensorMap& b,
+                          const CUtensorMap& o, const Params& p, cudaStream_t st) {
+  if (p.g.products == 1)
+    return idx64 ? launch<kEpi, __nv_bfloat16, int64_t, false>(a, b, o, p, st)
+                 : launch<kEpi, __nv_bfloat16, int32_t, false>(a, b, o, p, st);
+  return idx64 ? launch<kEpi, float, int64_t, true>(a, b, o, p, st)
+               : launch<kEpi, float, int32_t, true>(a, b, o, p, st);
 }
 
 cudaError_t launch_planes(const TableProblem& p, const void* src, long long rows,
@@ -698,9 +738,12 @@ cudaError_t launch_product(const Gemm& g, const CUtensorMap& a, const CUtensorMa
   Params p = {};
   p.g = g;
   p.err = err;
-  if (!f32) return launch<Epi::kStore, __nv_bfloat16, int32_t>(a, b, o, p, st);
-  return add ? launch<Epi::kAdd, float, int32_t>(a, b, o, p, st)
-             : launch<Epi::kStore, float, int32_t>(a, b, o, p, st);
+  if (!f32) return launch<Epi::kStore, __nv_bfloat16, int32_t, false>(a, b, o, p, st);
+  if (g.products == 1)
+    return add ? launch<Epi::kAdd, float, int32_t, false>(a, b, o, p, st)
+               : launch<Epi::kStore, float, int32_t, false>(a, b, o, p, st);
+  return add ? launch<Epi::kAdd, float, int32_t, true>(a, b, o, p, st)
+             : launch<Epi::kStore, float, int32_t, true>(a, b, o, p, st);
 }
 
 }  // namespace
@@ -742,7 +785,7 @@ cudaError_t launch_xent_tc(const TableProblem& p, const void* x, const void* tab
   if (!encode(&a, x, false, p.d, p.rows, planes, p.d, p.rows, kBlockK, 128) ||
       !encode(&b, table, false, p.d, p.vocab, planes, p.d, p.vocab, kBlockK, k.g.width / 2))
     return cudaErrorInvalidValue;
-  return launch_i<Epi::kLse, float>(p.idx64, a, b, a, k, st);
+  return launch_logits<Epi::kLse>(p.idx64, a, b, a, k, st);
 }
 
 size_t xent_tc_backward_bytes(const TableProblem& p) { return plan_backward(p).total; }
@@ -794,14 +837,13 @@ cudaError_t launch_xent_tc_backward(const TableProblem& p, const void* x, const 
         !encode(&g_out, gbuf, false, nv, p.rows, planes, plan.ld, p.rows, f32 ? 32 : 64, 32,
                 f32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B))
       return cudaErrorInvalidValue;
-    e = f32 ? launch_i<Epi::kGrad, float>(p.idx64, x_k, w_k, g_out, k, st)
-            : launch_i<Epi::kGrad, __nv_bfloat16>(p.idx64, x_k, w_k, g_out, k, st);
-    if (e) return e;
+    if ((e = launch_logits<Epi::kGrad>(p.idx64, x_k, w_k, g_out, k, st))) return e;
     // dx += g W
     Gemm gx = make_gemm(p.rows, p.d, nv, f32, false, true);
     // (a last, shorter piece may have blocks for fewer parts only)
     gx.kb_split = ceil_div(gx.kb, plan.dx_splits);
     gx.splits = ceil_div(gx.kb, gx.kb_split);
+    set_chunk(&gx);
     gx.items = gx.m_tiles * gx.n_tiles * gx.splits;
     void* dx_to = plan.sum_dx ? static_cast<void*>(dx_sums) : dx;
     if ((e = launch_product(gx, g_k, w_mn, dx_to, f32 || plan.sum_dx, p.d, p.rows, v0 > 0, err, st)))
@@ -810,6 +852,7 @@ cudaError_t launch_xent_tc_backward(const TableProblem& p, const void* x, const 
     Gemm gw = make_gemm(nv, p.d, (int)p.rows, f32, true, true);
     gw.splits = plan.dw_splits;
     gw.kb_split = ceil_div(gw.kb, gw.splits);
+    set_chunk(&gw);
     gw.items = gw.m_tiles * gw.n_tiles * gw.splits;
     char* dw_at = static_cast<char*>(dtable) + (size_t)v0 * p.d * p.elem();
     void* dw_to = plan.sum_dw ? static_cast<void*>(dw_sums) : dw_at;
