@@ -13,7 +13,6 @@ Build the library first:  python -m lsh_bucketed_sparse_b200.build
 
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import os
 import re
@@ -497,19 +496,32 @@ def make_route_shape(tokens, top_k, n_experts, d_model=8, dtype=torch.bfloat16,
                       dtype if isinstance(dtype, int) else _dtype_code(dtype), index_type, 0)
 
 
-@contextlib.contextmanager
-def _launching(device, stream):
+class _launching:
     """Makes ``device`` and ``stream`` current (the device's own current stream
     when None), so that what is allocated inside belongs to the stream the
-    kernels run on, and yields the stream's handle."""
-    with torch.cuda.device(device):
-        if stream is None:
-            yield ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
-            return
-        if stream.device != device:
+    kernels run on, and gives the stream's handle.  Costs nothing more where
+    the device is the current one already."""
+    __slots__ = ("device", "stream", "held")
+
+    def __init__(self, device, stream):
+        if stream is not None and stream.device != device:
             raise ValueError(f"stream is on {stream.device}, expected {device}")
-        with torch.cuda.stream(stream):
-            yield ctypes.c_void_p(stream.cuda_stream)
+        self.device, self.stream, self.held = device, stream, ()
+
+    def __enter__(self):
+        if self.stream is not None:
+            self.held = (torch.cuda.device(self.device), torch.cuda.stream(self.stream))
+        elif torch._C._cuda_getDevice() != self.device.index:
+            self.held = (torch.cuda.device(self.device),)
+        for h in self.held:
+            h.__enter__()
+        if self.stream is not None:
+            return self.stream.cuda_stream
+        return torch._C._cuda_getCurrentRawStream(self.device.index)
+
+    def __exit__(self, *exc):
+        for h in reversed(self.held):
+            h.__exit__(*exc)
 
 
 def _size(query, shape) -> int:
@@ -551,7 +563,7 @@ def lsh_attn_embed(tokens, table, *, scale=1.0, out=None, stream=None):
     shp = make_table_shape(tokens.numel(), V, D, table.dtype, _index_code(tokens, "tokens"), scale)
     with _launching(tokens.device, stream) as st:
         out = _out(out, "out", table.dtype, (*tokens.shape, D), tokens)
-        _check(lib().lsh_attn_embed(ctypes.byref(shp), _ptr(tokens), _ptr(table), _ptr(out), st))
+        _check(lib().lsh_attn_embed(ctypes.byref(shp), tokens.data_ptr(), table.data_ptr(), out.data_ptr(), st))
     return out
 
 
@@ -579,8 +591,8 @@ def lsh_attn_embed_backward(tokens, dout, vocab, *, scale=1.0, init=None, out=No
     with _launching(tokens.device, stream) as st:
         out = _out(out, "out", dout.dtype, (vocab, D), tokens)
         ws, n = _workspace(workspace, need, tokens)
-        _check(lib().lsh_attn_embed_backward(ctypes.byref(shp), _ptr(tokens), _ptr(dout),
-                                             _ptr(init), _ptr(out), _ptr(ws), _SZ(n), st))
+        _check(lib().lsh_attn_embed_backward(ctypes.byref(shp), tokens.data_ptr(), dout.data_ptr(),
+                                             (None if init is None else init.data_ptr()), out.data_ptr(), (None if ws is None else ws.data_ptr()), n, st))
     return out
 
 
@@ -611,8 +623,8 @@ def lsh_attn_xent(x, table, targets, *, scale=1.0, workspace=None, portable=Fals
         loss = _out(None, "loss", torch.float32, targets.shape, x)
         lse = _out(None, "lse", torch.float32, targets.shape, x)
         ws, n = _workspace(workspace, need, x)
-        _check(lib().lsh_attn_xent(ctypes.byref(shp), _ptr(x), _ptr(table), _ptr(targets),
-                                   _ptr(loss), _ptr(lse), _ptr(ws), _SZ(n), st))
+        _check(lib().lsh_attn_xent(ctypes.byref(shp), x.data_ptr(), table.data_ptr(), targets.data_ptr(),
+                                   loss.data_ptr(), lse.data_ptr(), (None if ws is None else ws.data_ptr()), n, st))
     return loss, lse
 
 
@@ -632,9 +644,9 @@ def lsh_attn_xent_backward(x, table, targets, lse, dloss, *, scale=1.0, workspac
         dx = _out(None, "dx", x.dtype, x.shape, x)
         dtable = _out(None, "dtable", x.dtype, table.shape, x)
         ws, n = _workspace(workspace, need, x)
-        _check(lib().lsh_attn_xent_backward(ctypes.byref(shp), _ptr(x), _ptr(table),
-                                            _ptr(targets), _ptr(lse), _ptr(dloss), _ptr(dx),
-                                            _ptr(dtable), _ptr(ws), _SZ(n), st))
+        _check(lib().lsh_attn_xent_backward(ctypes.byref(shp), x.data_ptr(), table.data_ptr(),
+                                            targets.data_ptr(), lse.data_ptr(), dloss.data_ptr(), dx.data_ptr(),
+                                            dtable.data_ptr(), (None if ws is None else ws.data_ptr()), n, st))
     return dx, dtable
 
 
@@ -659,8 +671,8 @@ def lsh_attn_route_sort(experts, n_experts, *, workspace=None, stream=None):
         undo = torch.empty(T, k, dtype=torch.int32, device=experts.device)
         offsets = torch.empty(n_experts + 1, dtype=torch.int32, device=experts.device)
         ws, n = _workspace(workspace, need, experts)
-        _check(lib().lsh_attn_route_sort(ctypes.byref(shp), _ptr(experts), _ptr(perm), _ptr(undo),
-                                         _ptr(offsets), _ptr(ws), _SZ(n), st))
+        _check(lib().lsh_attn_route_sort(ctypes.byref(shp), experts.data_ptr(), perm.data_ptr(), undo.data_ptr(),
+                                         offsets.data_ptr(), (None if ws is None else ws.data_ptr()), n, st))
     return perm, undo, offsets
 
 
@@ -686,8 +698,8 @@ def lsh_attn_route_gather(x, undo, offsets, *, out=None, stream=None):
     shp = _route_args(x, "x", False, undo, offsets)
     with _launching(x.device, stream) as st:
         out = _out(out, "out", x.dtype, (undo.numel(), x.shape[1]), x)
-        _check(lib().lsh_attn_route_gather(ctypes.byref(shp), _ptr(x), _ptr(undo), _ptr(offsets),
-                                           _ptr(out), st))
+        _check(lib().lsh_attn_route_gather(ctypes.byref(shp), x.data_ptr(), undo.data_ptr(), offsets.data_ptr(),
+                                           out.data_ptr(), st))
     return out
 
 
@@ -697,8 +709,8 @@ def lsh_attn_route_gather_backward(dxs, undo, offsets, *, out=None, stream=None)
     shp = _route_args(dxs, "dxs", True, undo, offsets)
     with _launching(dxs.device, stream) as st:
         out = _out(out, "out", dxs.dtype, (undo.shape[0], dxs.shape[1]), dxs)
-        _check(lib().lsh_attn_route_gather_backward(ctypes.byref(shp), _ptr(dxs), _ptr(undo),
-                                                    _ptr(offsets), _ptr(out), st))
+        _check(lib().lsh_attn_route_gather_backward(ctypes.byref(shp), dxs.data_ptr(), undo.data_ptr(),
+                                                    offsets.data_ptr(), out.data_ptr(), st))
     return out
 
 
@@ -709,8 +721,8 @@ def lsh_attn_route_combine(y, weights, undo, offsets, *, out=None, stream=None):
     _cuda(weights, "weights", torch.float32, undo.shape, y)
     with _launching(y.device, stream) as st:
         out = _out(out, "out", y.dtype, (undo.shape[0], y.shape[1]), y)
-        _check(lib().lsh_attn_route_combine(ctypes.byref(shp), _ptr(y), _ptr(weights), _ptr(undo),
-                                            _ptr(offsets), _ptr(out), st))
+        _check(lib().lsh_attn_route_combine(ctypes.byref(shp), y.data_ptr(), weights.data_ptr(), undo.data_ptr(),
+                                            offsets.data_ptr(), out.data_ptr(), st))
     return out
 
 
@@ -723,7 +735,7 @@ def lsh_attn_route_combine_backward(dout, y, weights, undo, offsets, *, stream=N
     with _launching(y.device, stream) as st:
         dy = torch.empty_like(y)
         dw = torch.empty_like(weights)
-        _check(lib().lsh_attn_route_combine_backward(ctypes.byref(shp), _ptr(dout), _ptr(y),
-                                                     _ptr(weights), _ptr(undo), _ptr(offsets),
-                                                     _ptr(dy), _ptr(dw), st))
+        _check(lib().lsh_attn_route_combine_backward(ctypes.byref(shp), dout.data_ptr(), y.data_ptr(),
+                                                     weights.data_ptr(), undo.data_ptr(), offsets.data_ptr(),
+                                                     dy.data_ptr(), dw.data_ptr(), st))
     return dy, dw

@@ -8,10 +8,10 @@
 // Gradient: the tokens are ordered by id (key_sort.cu), so a table row's sum
 // runs over consecutive slots and is written once, without atomics: the sum's
 // order is fixed by the input alone.  Sums are float32 and rounded once.  A
-// run of up to kChunk slots is summed by the lanes that own the row.  Longer
-// runs (frequent tokens) are cut at multiples of kChunk: one CTA per chunk
-// leaves a float32 partial sum, and a second kernel adds a run's partial
-// sums in order.
+// run of up to kChunk slots is summed by the threads that own the row's
+// pieces.  Longer runs (frequent tokens) are cut at multiples of kChunk: one
+// CTA per chunk leaves a float32 partial sum, and the last of a run's CTAs to
+// finish adds them in order.
 #include "common.cuh"
 #include "internal.h"
 #include "vec16.cuh"
@@ -22,6 +22,9 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kChunk = 64;  // longest run summed in one go
 
+// A thread takes kPieces pieces, kThreads apart: its tokens, then its rows are
+// under way together.
+constexpr int kPieces = 4;
 template <typename T, typename I>
 __global__ void __launch_bounds__(kThreads)
 embed_kernel(const I* __restrict__ tokens, const T* __restrict__ table, T* __restrict__ out,
@@ -29,38 +32,98 @@ embed_kernel(const I* __restrict__ tokens, const T* __restrict__ table, T* __res
   using V = Vec16<T>;
   wait_prior_grid();
   const int per_row = d / V::N;
-  const long long p = (long long)blockIdx.x * kThreads + threadIdx.x;
-  if (p >= pieces) return;
-  const long long row = p / per_row;
-  const int col = (int)(p - row * per_row) * V::N;
-  const I tok = tokens[row];
-  float f[V::N];
+  const PieceBlock at(blockIdx.x, kThreads * kPieces, per_row);
+  int col[kPieces];
+  I tok[kPieces];
+  uint4 v[kPieces];
 #pragma unroll
-  for (int t = 0; t < V::N; ++t) f[t] = 0.f;
-  if (tok >= 0 && tok < (I)vocab) {
-    V::load(table + (size_t)tok * d + col, f);
-#pragma unroll
-    for (int t = 0; t < V::N; ++t) f[t] *= scale;
+  for (int u = 0; u < kPieces; ++u) {
+    long long row;
+    at.locate(u * kThreads + threadIdx.x, per_row, &row, &col[u]);
+    tok[u] = at.first + u * kThreads + threadIdx.x < pieces ? tokens[row] : (I)-1;
   }
-  V::store(out + (size_t)row * d + col, f);
+#pragma unroll
+  for (int u = 0; u < kPieces; ++u) {
+    v[u] = make_uint4(0, 0, 0, 0);
+    if (tok[u] >= 0 && tok[u] < (I)vocab)
+      v[u] = V::raw(table + (size_t)tok[u] * d + col[u] * V::N);
+  }
+#pragma unroll
+  for (int u = 0; u < kPieces; ++u) {
+    const long long p = at.first + u * kThreads + threadIdx.x;
+    if (p >= pieces) continue;
+    float f[V::N];
+    V::unpack(v[u], f);
+    if (tok[u] >= 0 && tok[u] < (I)vocab) {
+#pragma unroll
+      for (int t = 0; t < V::N; ++t) f[t] *= scale;
+    }
+    V::store(out + p * V::N, f);
+  }
 }
 
 __device__ __forceinline__ bool frequent(int2 run) { return run.y - run.x > kChunk; }
 
+// Threads that share a row of float32 partial sums, four columns each.
+__device__ __forceinline__ int width4(int width, int d) {
+  while (width < kThreads && width * 4 < d) width *= 2;
+  return width;
+}
+
+// Sum of `count` rows of `d` values, row i at src(i), over the block:
+// `width` threads (a power of two) share a row, the block's kThreads / width
+// groups share the rows, and the groups' sums are added in order.  The block's
+// first `width` threads get the values; emit(col, values) is called for their
+// columns.
+template <int N, typename Load, typename Emit>
+__device__ void block_sum_rows(int count, int d, int width, float* sums, Load load, Emit emit) {
+  const int groups = kThreads / width, grp = threadIdx.x / width, at = threadIdx.x & (width - 1);
+  for (int col0 = 0; col0 < d; col0 += width * N) {
+    const int col = col0 + at * N;
+    float a[N];
+#pragma unroll
+    for (int t = 0; t < N; ++t) a[t] = 0.f;
+    if (col < d) {
+#pragma unroll 8
+      for (int s = grp; s < count; s += groups) {
+        float f[N];
+        load(s, col, f);
+#pragma unroll
+        for (int t = 0; t < N; ++t) a[t] += f[t];
+      }
+    }
+    if (groups > 1) {
+#pragma unroll
+      for (int t = 0; t < N; ++t) sums[t * kThreads + threadIdx.x] = a[t];
+      __syncthreads();
+      if (grp == 0)
+        for (int o = 1; o < groups; ++o)
+#pragma unroll
+          for (int t = 0; t < N; ++t) a[t] += sums[t * kThreads + o * width + at];
+      __syncthreads();
+    }
+    if (grp == 0 && col < d) emit(col, a);
+  }
+}
+
 // Blocks [0, chunks): the chunk's partial sums of frequent tokens, at most
 // two (the run of its first slot -> part[chunk][0], another run that reaches
-// past its end -> part[chunk][1]).  Later blocks: one table row per group of
-// lanes, for rows that are not frequent.
+// past its end -> part[chunk][1]).  The block that completes a run's partial
+// sums (arrived[], counted at the run's first chunk) adds them in their order
+// and writes the table's row.  Later blocks: one 16-byte piece of a table row
+// per thread, for rows that are not frequent.
 template <typename T>
 __global__ void __launch_bounds__(kThreads)
 embed_grad_kernel(const int32_t* __restrict__ perm, const int32_t* __restrict__ sorted,
                   const int2* __restrict__ runs, const T* __restrict__ dout, const T* init,
-                  T* dtable, float* __restrict__ part, int n, int chunks, int vocab, int d,
-                  int lanes, float scale) {
+                  T* dtable, float* part, int32_t* arrived, int n, int chunks, int vocab, int d,
+                  int width, float scale) {
   using V = Vec16<T>;
   wait_prior_grid();
   if ((int)blockIdx.x < chunks) {
     __shared__ int32_t rows[kChunk];
+    __shared__ float sums[kThreads * V::N];
+    __shared__ int last;
     const int c0 = blockIdx.x * kChunk, c1 = min(n, c0 + kChunk);
     const int k0 = sorted[c0], k1 = sorted[c1 - 1];
     const int2 r0 = k0 < vocab ? runs[k0] : make_int2(0, 0);
@@ -73,112 +136,80 @@ embed_grad_kernel(const int32_t* __restrict__ perm, const int32_t* __restrict__ 
       if (!frequent(r)) continue;
       const int b = max(r.x, c0) - c0, e = min(r.y, c1) - c0;
       float* to = part + ((size_t)blockIdx.x * 2 + which) * d;
-      for (int col = threadIdx.x * 4; col < d; col += kThreads * 4) {
-        float a[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 8
-        for (int s = b; s < e; ++s) {
-          const T* x = dout + (size_t)rows[s] * d + col;
+      block_sum_rows<V::N>(
+          e - b, d, width, sums,
+          [&](int s, int col, float* f) { V::load(dout + (size_t)rows[b + s] * d + col, f); },
+          [&](int col, const float* a) {
 #pragma unroll
-          for (int t = 0; t < 4; ++t) a[t] += to_f32(x[t]);
-        }
-        *reinterpret_cast<float4*>(to + col) = make_float4(a[0], a[1], a[2], a[3]);
-      }
+            for (int t = 0; t < V::N; t += 4)
+              *reinterpret_cast<float4*>(to + col + t) =
+                  make_float4(a[t], a[t + 1], a[t + 2], a[t + 3]);
+          });
+      const int first = r.x / kChunk, count = (r.y - 1) / kChunk - first + 1;
+      __threadfence();
+      __syncthreads();
+      if (threadIdx.x == 0) last = atomicAdd(&arrived[first], 1) == count - 1;
+      __syncthreads();
+      if (!last) continue;
+      __threadfence();
+      const size_t row = (size_t)(which ? k1 : k0) * d;
+      const bool shared = r.x > first * kChunk;  // the first chunk begins with another run
+      block_sum_rows<4>(
+          count, d, width4(width, d), sums,
+          [&](int c, int col, float* f) {
+            const size_t at = ((size_t)(first + c) * 2 + (c == 0 && shared)) * d + col;
+            const float4 x = __ldcg(reinterpret_cast<const float4*>(part + at));
+            f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
+          },
+          [&](int col, const float* a) {
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+              dtable[row + col + t] =
+                  from_f32<T>(a[t] * scale + (init ? to_f32(init[row + col + t]) : 0.f));
+          });
     }
     return;
   }
-  const int per_block = kThreads / lanes;
-  const long long v =
-      (long long)(blockIdx.x - chunks) * per_block + threadIdx.x / lanes;
+  const int per_row = d / V::N;
+  const PieceBlock at(blockIdx.x - chunks, kThreads, per_row);
+  long long v;
+  int col;
+  at.locate(threadIdx.x, per_row, &v, &col);
   if (v >= vocab) return;
+  col *= V::N;
+  uint4 old = make_uint4(0, 0, 0, 0);
+  if (init) old = V::raw(init + (size_t)v * d + col);
   const int2 r = runs[v];
   if (frequent(r)) return;
-  for (int col = (threadIdx.x % lanes) * V::N; col < d; col += lanes * V::N) {
-    float a[V::N];
+  float a[V::N];
 #pragma unroll
-    for (int t = 0; t < V::N; ++t) a[t] = 0.f;
+  for (int t = 0; t < V::N; ++t) a[t] = 0.f;
 #pragma unroll 4
-    for (int s = r.x; s < r.y; ++s) {
-      float f[V::N];
-      V::load(dout + (size_t)perm[s] * d + col, f);
+  for (int s = r.x; s < r.y; ++s) {
+    float f[V::N];
+    V::load(dout + (size_t)perm[s] * d + col, f);
 #pragma unroll
-      for (int t = 0; t < V::N; ++t) a[t] += f[t];
-    }
-#pragma unroll
-    for (int t = 0; t < V::N; ++t) a[t] *= scale;
-    if (init) {
-      float f[V::N];
-      V::load(init + (size_t)v * d + col, f);
-#pragma unroll
-      for (int t = 0; t < V::N; ++t) a[t] += f[t];
-    }
-    V::store(dtable + (size_t)v * d + col, a);
+    for (int t = 0; t < V::N; ++t) a[t] += f[t];
   }
-}
-
-// Grid (chunks, columns / kColumns): the CTA of the chunk in which a frequent
-// run begins (at most one does: it reaches past the chunk's end) adds the
-// run's partial sums, each warp every kSumWarps-th, then the warps' sums in
-// order.
-constexpr int kColumns = 128, kSumWarps = 8;
-template <typename T>
-__global__ void __launch_bounds__(kSumWarps * 32)
-embed_grad_long_kernel(const int32_t* __restrict__ sorted, const int2* __restrict__ runs,
-                       const float* __restrict__ part, const T* init, T* dtable, int n, int vocab,
-                       int d, float scale) {
-  __shared__ float4 sums[kSumWarps][32];
-  wait_prior_grid();
-  const int c0 = blockIdx.x * kChunk, c1 = min(n, c0 + kChunk);
-  const int v = sorted[c1 - 1];
-  if (v >= vocab) return;
-  const int2 r = runs[v];
-  if (!frequent(r) || r.x < c0) return;
-  const int last = (r.y - 1) / kChunk;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int col = blockIdx.y * kColumns + lane * 4;
-  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (col < d) {
-#pragma unroll 4
-    for (int c = (int)blockIdx.x + warp; c <= last; c += kSumWarps) {
-      const int which = c == (int)blockIdx.x && r.x > c0;
-      const float4 x = *reinterpret_cast<const float4*>(part + ((size_t)c * 2 + which) * d + col);
-      a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
-    }
-  }
-  sums[warp][lane] = a;
-  __syncthreads();
-  if (warp != 0 || col >= d) return;
+  float f[V::N];
+  V::unpack(old, f);
 #pragma unroll
-  for (int w = 1; w < kSumWarps; ++w) {
-    const float4 x = sums[w][lane];
-    a.x += x.x; a.y += x.y; a.z += x.z; a.w += x.w;
-  }
-  const float f[4] = {a.x, a.y, a.z, a.w};
-  const size_t at = (size_t)v * d + col;
-#pragma unroll
-  for (int t = 0; t < 4; ++t)
-    dtable[at + t] = from_f32<T>(f[t] * scale + (init ? to_f32(init[at + t]) : 0.f));
+  for (int t = 0; t < V::N; ++t) a[t] = a[t] * scale + f[t];
+  V::store(dtable + (size_t)v * d + col, a);
 }
 
 template <typename T>
 cudaError_t grad_t(const TableProblem& p, const int32_t* perm, const int32_t* sorted,
                    const int2* runs, const void* dout, const void* init, void* dtable, float* part,
-                   cudaStream_t st) {
-  const int chunks = (int)((p.rows + kChunk - 1) / kChunk);
-  int lanes = 1;
-  while (lanes < 32 && lanes * Vec16<T>::N < p.d) lanes *= 2;
-  const long long blocks = chunks + ((long long)p.vocab * lanes + kThreads - 1) / kThreads;
-  const T* g = static_cast<const T*>(dout);
-  const T* in = static_cast<const T*>(init);
-  T* out = static_cast<T*>(dtable);
+                   int32_t* arrived, int chunks, cudaStream_t st) {
+  int width = 1;
+  while (width < kThreads && width * Vec16<T>::N < p.d) width *= 2;
+  const long long blocks =
+      chunks + ((long long)p.vocab * (p.d / Vec16<T>::N) + kThreads - 1) / kThreads;
   cudaError_t e = launch_dependent(embed_grad_kernel<T>, dim3((unsigned)blocks), dim3(kThreads), 0,
-                                   st, perm, sorted, runs, g, in, out, part, (int)p.rows, chunks,
-                                   p.vocab, p.d, lanes, p.scale);
-  if (e) return e;
-  note_launch();
-  if (p.rows <= kChunk) return cudaSuccess;  // no run is that long
-  e = launch_dependent(embed_grad_long_kernel<T>, dim3(chunks, (p.d + kColumns - 1) / kColumns),
-                       dim3(kSumWarps * 32), 0, st, sorted, runs, static_cast<const float*>(part),
-                       in, out, (int)p.rows, p.vocab, p.d, p.scale);
+                                   st, perm, sorted, runs, static_cast<const T*>(dout),
+                                   static_cast<const T*>(init), static_cast<T*>(dtable), part,
+                                   arrived, (int)p.rows, chunks, p.vocab, p.d, width, p.scale);
   if (e) return e;
   note_launch();
   return cudaSuccess;
@@ -215,8 +246,9 @@ cudaError_t embed_t(const TableProblem& p, const void* tokens, const void* table
                     cudaStream_t st) {
   const long long pieces = p.rows * (p.d / Vec16<T>::N);
   cudaError_t e = launch_dependent(
-      embed_kernel<T, I>, dim3((unsigned)((pieces + kThreads - 1) / kThreads)), dim3(kThreads), 0,
-      st, static_cast<const I*>(tokens), static_cast<const T*>(table), static_cast<T*>(out),
+      embed_kernel<T, I>,
+      dim3((unsigned)((pieces + kThreads * kPieces - 1) / (kThreads * kPieces))), dim3(kThreads), 0, st,
+      static_cast<const I*>(tokens), static_cast<const T*>(table), static_cast<T*>(out),
       pieces, p.vocab, p.d, p.scale);
   if (e) return e;
   note_launch();
@@ -226,7 +258,8 @@ cudaError_t embed_t(const TableProblem& p, const void* tokens, const void* table
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 struct Scratch {
-  size_t perm, sorted, runs, part, sort, total;
+  int chunks;  // none where no run can be that long
+  size_t perm, sorted, runs, part, arrived, sort, total;
 };
 
 Scratch scratch_layout(const TableProblem& p) {
@@ -236,8 +269,9 @@ Scratch scratch_layout(const TableProblem& p) {
   s.perm = off;   off += align256(n * sizeof(int32_t));
   s.sorted = off; off += align256(n * sizeof(int32_t));
   s.runs = off;   off += align256((size_t)p.vocab * sizeof(int2));
-  s.part = off;
-  if (p.rows > kChunk) off += align256((n + kChunk - 1) / kChunk * 2 * p.d * sizeof(float));
+  s.chunks = p.rows > kChunk ? (int)((n + kChunk - 1) / kChunk) : 0;
+  s.part = off;   off += align256((size_t)s.chunks * 2 * p.d * sizeof(float));
+  s.arrived = off; off += align256((size_t)s.chunks * sizeof(int32_t));
   s.sort = off;   off += key_sort_scratch_bytes(p.rows, p.vocab);
   s.total = off;
   return s;
@@ -272,11 +306,14 @@ cudaError_t launch_embed_backward(const TableProblem& p, const void* tokens, con
   int32_t* sorted = reinterpret_cast<int32_t*>(base + s.sorted);
   int2* runs = reinterpret_cast<int2*>(base + s.runs);
   float* part = reinterpret_cast<float*>(base + s.part);
+  int32_t* arrived = reinterpret_cast<int32_t*>(base + s.arrived);
   cudaError_t e = launch_key_sort(p.rows, p.vocab, tokens, p.idx64, perm, nullptr, nullptr, sorted,
-                                  runs, base + s.sort, st);
+                                  runs, arrived, s.chunks, base + s.sort, st);
   if (e) return e;
-  return p.bf16 ? grad_t<__nv_bfloat16>(p, perm, sorted, runs, dout, init, dtable, part, st)
-                : grad_t<float>(p, perm, sorted, runs, dout, init, dtable, part, st);
+  return p.bf16 ? grad_t<__nv_bfloat16>(p, perm, sorted, runs, dout, init, dtable, part, arrived,
+                                        s.chunks, st)
+                : grad_t<float>(p, perm, sorted, runs, dout, init, dtable, part, arrived, s.chunks,
+                                st);
 }
 
 }  // namespace lsh

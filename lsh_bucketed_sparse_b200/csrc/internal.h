@@ -123,11 +123,12 @@ cudaError_t launch_combine(const Problem& p, const void* o_rounds, const float* 
 // Keys outside [0, K) come last.  perm[s]: the entry in slot s; undo (may be
 // NULL) its inverse; offsets (may be NULL; K < 1024 only) [K + 1]: each key's
 // first slot, offsets[K] the first slot of the keys outside; with runs (may be
-// NULL), sorted[n] gets the keys in order and runs[K] each key's slots [x, y).
+// NULL), sorted[n] gets the keys in order and runs[K] each key's slots [x, y),
+// and zeros[0, n_zeros) is cleared (n_zeros <= n).
 size_t key_sort_scratch_bytes(long long n, int K);
 cudaError_t launch_key_sort(long long n, int K, const void* keys, bool keys64, int32_t* perm,
                             int32_t* undo, int32_t* offsets, int32_t* sorted, int2* runs,
-                            void* scratch, cudaStream_t st);
+                            int32_t* zeros, int n_zeros, void* scratch, cudaStream_t st);
 
 // ---- the token table: lookup, its gradient, cross entropy -----------------------
 // Validated copy of lsh_table.

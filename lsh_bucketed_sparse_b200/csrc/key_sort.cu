@@ -8,7 +8,9 @@
 // pass cuts the entries into tiles of kTile:
 //   count    one CTA per tile: its entries per digit value;
 //   scan     one CTA: per digit value the exclusive sum over the tiles, then
-//            the first slot of every value (their exclusive sum);
+//            the first slot of every value (their exclusive sum); up to
+//            kFusedTiles tiles each CTA of the scatter does it for itself, and
+//            with one tile there is nothing to count before either;
 //   scatter  one CTA per tile, each warp a contiguous part of it: entries of
 //            equal digit in a warp are ranked by their lane, in the tile by
 //            their warp, so equal digits keep their order without atomics
@@ -26,6 +28,7 @@ constexpr int kPer = kTile / kThreads;      // entries per thread
 constexpr int kScanThreads = 1024;
 constexpr int kOneDigitBits = 10;
 constexpr int kMaxBins = 1 << 11;
+constexpr int kFusedTiles = 64;
 
 struct Plan {
   int bits, lo, hi;  // hi == 0: one digit of `lo` = `bits` bits
@@ -96,11 +99,13 @@ key_count_kernel(const S src, int32_t* __restrict__ cnt, int2* __restrict__ runs
   for (int b = threadIdx.x; b < bins; b += kThreads) cnt[(size_t)blockIdx.x * bins + b] = hist[b];
 }
 
-// Exclusive scan of a[0..n) (shared memory) by the block; returns nothing.
+// Exclusive scan of a[0..n) (shared memory) by a block of kBlock threads.
+template <int kBlock>
 __device__ void block_scan(int32_t* a, int n) {
-  __shared__ int32_t warp_tot[kScanThreads / 32];
+  constexpr int kBlockWarps = kBlock / 32;
+  __shared__ int32_t warp_tot[kBlockWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int per = (n + kScanThreads - 1) / kScanThreads;
+  const int per = (n + kBlock - 1) / kBlock;
   const int lo = min(n, tid * per), hi = min(n, lo + per);
   int32_t local = 0;
   for (int t = lo; t < hi; ++t) local += a[t];
@@ -113,14 +118,14 @@ __device__ void block_scan(int32_t* a, int n) {
   if (lane == 31) warp_tot[warp] = incl;
   __syncthreads();
   if (warp == 0) {
-    const int32_t w = warp_tot[lane];
+    const int32_t w = lane < kBlockWarps ? warp_tot[lane] : 0;
     int32_t wi = w;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int32_t y = __shfl_up_sync(0xffffffffu, wi, o);
       if (lane >= o) wi += y;
     }
-    warp_tot[lane] = wi - w;
+    if (lane < kBlockWarps) warp_tot[lane] = wi - w;
   }
   __syncthreads();
   int32_t run = warp_tot[warp] + incl - local;
@@ -156,7 +161,7 @@ key_scan_kernel(int32_t* __restrict__ cnt, int32_t* __restrict__ base_out,
     base[b] = run;
   }
   __syncthreads();
-  block_scan(base, bins);
+  block_scan<kScanThreads>(base, bins);
   for (int b = threadIdx.x; b < bins; b += kScanThreads) {
     base_out[b] = base[b];
     if (offsets) offsets[b] = base[b];
@@ -164,26 +169,34 @@ key_scan_kernel(int32_t* __restrict__ cnt, int32_t* __restrict__ base_out,
 }
 
 // perm / undo / sorted: any may be NULL.  sorted[s] is the whole key in slot s.
-template <typename S>
+// kScanned: cnt and base come from the scan kernel.  Otherwise cnt holds the
+// tiles' plain counts (not read when there is one tile) and every CTA adds up
+// for itself what stands before it.
+template <typename S, bool kScanned>
 __global__ void __launch_bounds__(kThreads)
 key_scatter_kernel(const S src, const int32_t* __restrict__ cnt, const int32_t* __restrict__ base,
                    int32_t* __restrict__ perm, int32_t* __restrict__ undo,
-                   int32_t* __restrict__ sorted, int n, int bins, int bits, int shift,
-                   int mask) {
-  extern __shared__ int32_t off[];  // [kWarps][bins]
+                   int32_t* __restrict__ sorted, int32_t* __restrict__ offsets,
+                   int2* __restrict__ runs, int n_runs, int n, int tiles, int bins, int bits,
+                   int shift, int mask) {
+  extern __shared__ int32_t off[];  // [kWarps][bins], then without kScanned first[bins], before[bins]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int32_t* mine = off + (size_t)warp * bins;
   for (int b = lane; b < bins; b += 32) mine[b] = 0;
   wait_prior_grid();
   constexpr int kRows = kTile / kWarps / 32;
   const int beg = blockIdx.x * kTile + warp * (kTile / kWarps);
-  int key[kRows];
+  int key[kRows], entry[kRows];
   unsigned peers[kRows];
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
     const int e = beg + 32 * i + lane;
     key[i] = e < n ? src.key(e) : -1;
+    entry[i] = e < n ? src.entry(e) : 0;
   }
+  // (with one tile there was no count kernel to empty the runs)
+  for (int v = blockIdx.x * kThreads + threadIdx.x; v < n_runs; v += gridDim.x * kThreads)
+    runs[v] = make_int2(0, 0);
   __syncwarp();
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
@@ -201,9 +214,39 @@ key_scatter_kernel(const S src, const int32_t* __restrict__ cnt, const int32_t* 
     __syncwarp();
   }
   __syncthreads();
+  int32_t* first = off + (size_t)kWarps * bins;
+  int32_t* before = first + bins;
+  if constexpr (!kScanned) {
+    constexpr int kAhead = 16;  // tiles loaded before any is used
+    for (int b = threadIdx.x; b < bins; b += kThreads) {
+      int32_t pre = 0, all = 0;
+      if (tiles == 1) {
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) all += off[(size_t)w * bins + b];
+      } else {
+        for (int t0 = 0; t0 < tiles; t0 += kAhead) {
+          int32_t x[kAhead];
+#pragma unroll
+          for (int k = 0; k < kAhead; ++k)
+            x[k] = t0 + k < tiles ? cnt[(size_t)(t0 + k) * bins + b] : 0;
+#pragma unroll
+          for (int k = 0; k < kAhead; ++k) {
+            if (t0 + k < (int)blockIdx.x) pre += x[k];
+            all += x[k];
+          }
+        }
+      }
+      first[b] = all;
+      before[b] = pre;
+    }
+    __syncthreads();
+    block_scan<kThreads>(first, bins);
+    if (offsets && blockIdx.x == 0)
+      for (int b = threadIdx.x; b < bins; b += kThreads) offsets[b] = first[b];
+  }
   const int32_t* c = cnt + (size_t)blockIdx.x * bins;
   for (int b = threadIdx.x; b < bins; b += kThreads) {
-    int32_t run = base[b] + c[b];
+    int32_t run = kScanned ? base[b] + c[b] : first[b] + before[b];
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
       const int32_t x = off[(size_t)w * bins + b];
@@ -214,16 +257,14 @@ key_scatter_kernel(const S src, const int32_t* __restrict__ cnt, const int32_t* 
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
-    const int e = beg + 32 * i + lane;
     const bool valid = key[i] >= 0;
     const int dg = (key[i] >> shift) & mask;
     int slot = 0;
     if (valid) slot = mine[dg] + __popc(peers[i] & ((1u << lane) - 1u));
     __syncwarp();
     if (valid) {
-      const int entry = src.entry(e);
-      if (perm) perm[slot] = entry;
-      if (undo) undo[entry] = slot;
+      if (perm) perm[slot] = entry[i];
+      if (undo) undo[entry[i]] = slot;
       if (sorted) sorted[slot] = key[i];
       if (lane == 31 - __clz(peers[i])) mine[dg] += __popc(peers[i]);
     }
@@ -231,12 +272,15 @@ key_scatter_kernel(const S src, const int32_t* __restrict__ cnt, const int32_t* 
   }
 }
 
-// runs[v] = the slots [x, y) that hold key v, where there are any.
+// runs[v] = the slots [x, y) that hold key v, where there are any; zeros[0,
+// n_zeros) = 0 for the kernel after (n_zeros <= n).
 __global__ void __launch_bounds__(kThreads)
-key_runs_kernel(const int32_t* __restrict__ sorted, int2* __restrict__ runs, int n, int K) {
+key_runs_kernel(const int32_t* __restrict__ sorted, int2* __restrict__ runs,
+                int32_t* __restrict__ zeros, int n_zeros, int n, int K) {
   wait_prior_grid();
   const int s = blockIdx.x * kThreads + threadIdx.x;
   if (s >= n) return;
+  if (s < n_zeros) zeros[s] = 0;
   const int k = sorted[s];
   if (k >= K) return;
   if (s == 0 || sorted[s - 1] != k) runs[k].x = s;
@@ -254,8 +298,8 @@ Scratch scratch_layout(long long n, const Plan& p) {
   const int bins = p.bins_lo > p.bins_hi ? p.bins_lo : p.bins_hi;
   Scratch s;
   size_t off = 0;
-  s.cnt = off;  off += align256((size_t)p.tiles * bins * sizeof(int32_t));
-  s.base = off; off += align256((size_t)bins * sizeof(int32_t));
+  s.cnt = off;  off += p.tiles > 1 ? align256((size_t)p.tiles * bins * sizeof(int32_t)) : 0;
+  s.base = off; off += p.tiles > kFusedTiles ? align256((size_t)bins * sizeof(int32_t)) : 0;
   s.keys = off; off += p.hi ? align256((size_t)n * sizeof(int32_t)) : 0;
   s.entries = off; off += p.hi ? align256((size_t)n * sizeof(int32_t)) : 0;
   s.total = off;
@@ -268,23 +312,30 @@ cudaError_t one_pass(const S& src, int32_t* cnt, int32_t* base, int32_t* offsets
                      int bins, int bits, int shift, cudaStream_t st) {
   const int mask = (1 << bits) - 1;
   const size_t row = (size_t)bins * sizeof(int32_t);
+  const bool fused = tiles <= kFusedTiles;
   cudaError_t e;
-  if (kWarps * row > 48 * 1024 &&
-      (e = cudaFuncSetAttribute(key_scatter_kernel<S>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                (int)(kWarps * row))))
+  if (tiles > 1) {
+    if ((e = launch_dependent(key_count_kernel<S>, dim3(tiles), dim3(kThreads), row, st, src, cnt,
+                              runs, n_runs, n, bins, shift, mask)))
+      return e;
+    note_launch();
+    n_runs = 0;
+  }
+  if (!fused) {
+    if ((e = launch_dependent(key_scan_kernel, dim3(1), dim3(kScanThreads), row, st, cnt, base,
+                              offsets, bins, tiles)))
+      return e;
+    note_launch();
+  }
+  auto kernel = fused ? key_scatter_kernel<S, false> : key_scatter_kernel<S, true>;
+  const size_t smem = (kWarps + (fused ? 2 : 0)) * row;
+  if (smem > 48 * 1024 &&
+      (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)))
     return e;
-  if ((e = launch_dependent(key_count_kernel<S>, dim3(tiles), dim3(kThreads), row, st, src, cnt,
-                            runs, n_runs, n, bins, shift, mask)))
-    return e;
-  note_launch();
-  if ((e = launch_dependent(key_scan_kernel, dim3(1), dim3(kScanThreads), row, st, cnt, base,
-                            offsets, bins, tiles)))
-    return e;
-  note_launch();
-  if ((e = launch_dependent(key_scatter_kernel<S>, dim3(tiles), dim3(kThreads), kWarps * row, st,
-                            src, static_cast<const int32_t*>(cnt),
-                            static_cast<const int32_t*>(base), perm, undo, sorted, n, bins, bits,
-                            shift, mask)))
+  if ((e = launch_dependent(kernel, dim3(tiles), dim3(kThreads), smem, st, src,
+                            static_cast<const int32_t*>(cnt), static_cast<const int32_t*>(base),
+                            perm, undo, sorted, offsets, runs, n_runs, n, tiles, bins, bits, shift,
+                            mask)))
     return e;
   note_launch();
   return cudaSuccess;
@@ -298,7 +349,7 @@ size_t key_sort_scratch_bytes(long long n, int K) {
 
 cudaError_t launch_key_sort(long long n_, int K, const void* keys, bool keys64, int32_t* perm,
                             int32_t* undo, int32_t* offsets, int32_t* sorted, int2* runs,
-                            void* scratch, cudaStream_t st) {
+                            int32_t* zeros, int n_zeros, void* scratch, cudaStream_t st) {
   const Plan p = make_plan(n_, K);
   if (p.bins_lo > kMaxBins || p.bins_hi > kMaxBins || n_ < 1) return cudaErrorInvalidValue;
   if (offsets && p.hi) return cudaErrorInvalidValue;
@@ -328,8 +379,8 @@ cudaError_t launch_key_sort(long long n_, int K, const void* keys, bool keys64, 
   }
   if (runs) {
     if ((e = launch_dependent(key_runs_kernel, dim3((n + kThreads - 1) / kThreads),
-                              dim3(kThreads), 0, st, static_cast<const int32_t*>(sorted), runs, n,
-                              K)))
+                              dim3(kThreads), 0, st, static_cast<const int32_t*>(sorted), runs,
+                              zeros, n_zeros, n, K)))
       return e;
     note_launch();
   }

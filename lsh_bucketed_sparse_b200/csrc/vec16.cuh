@@ -43,4 +43,29 @@ template <> struct Vec16<__nv_bfloat16> {
   }
 };
 
+// A block's share of the pieces of a matrix, in row-major order: one 64-bit
+// division for the block, a 32-bit one per piece.
+struct PieceBlock {
+  long long first, row0;
+  unsigned rem;
+  __device__ PieceBlock(unsigned block, unsigned size, int per_row) {
+    first = (long long)block * size;
+    row0 = first / per_row;
+    rem = (unsigned)(first - row0 * per_row);
+  }
+  // Row and piece in the row of the block's i-th piece.
+  __device__ void locate(unsigned i, int per_row, long long* row, int* piece) const {
+    const unsigned q = rem + i, r = q / (unsigned)per_row;
+    *row = row0 + r;
+    *piece = (int)(q - r * (unsigned)per_row);
+  }
+};
+
+// Lanes that share a row of `pieces` pieces: a power of two, 32 at most.
+inline int lanes_of_row(int pieces) {
+  int lanes = 1;
+  while (lanes < 32 && lanes < pieces) lanes *= 2;
+  return lanes;
+}
+
 }  // namespace lsh
