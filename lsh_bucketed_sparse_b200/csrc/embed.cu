@@ -110,14 +110,18 @@ __device__ void block_sum_rows(int count, int d, int width, float* sums, Load lo
 // two (the run of its first slot -> part[chunk][0], another run that reaches
 // past its end -> part[chunk][1]).  The block that completes a run's partial
 // sums (arrived[], counted at the run's first chunk) adds them in their order
-// and writes the table's row.  Later blocks: one 16-byte piece of a table row
-// per thread, for rows that are not frequent.
-template <typename T>
+// and writes the table's row.  Later blocks: kRows table rows per group of
+// `lanes` lanes (a power of two), for rows that are not frequent: the runs and
+// first entries of all of them are read at once; U pieces of a row are under
+// way at a time where it has one entry at most, four entries of a piece where
+// it has more.
+constexpr int kRows = 4;
+template <typename T, int U>
 __global__ void __launch_bounds__(kThreads)
 embed_grad_kernel(const int32_t* __restrict__ perm, const int32_t* __restrict__ sorted,
                   const int2* __restrict__ runs, const T* __restrict__ dout, const T* init,
                   T* dtable, float* part, int32_t* arrived, int n, int chunks, int vocab, int d,
-                  int width, float scale) {
+                  int lanes, int width, float scale) {
   using V = Vec16<T>;
   wait_prior_grid();
   if ((int)blockIdx.x < chunks) {
@@ -170,46 +174,76 @@ embed_grad_kernel(const int32_t* __restrict__ perm, const int32_t* __restrict__ 
     }
     return;
   }
-  const int per_row = d / V::N;
-  const PieceBlock at(blockIdx.x - chunks, kThreads, per_row);
-  long long v;
-  int col;
-  at.locate(threadIdx.x, per_row, &v, &col);
-  if (v >= vocab) return;
-  col *= V::N;
-  uint4 old = make_uint4(0, 0, 0, 0);
-  if (init) old = V::raw(init + (size_t)v * d + col);
-  const int2 r = runs[v];
-  if (frequent(r)) return;
-  float a[V::N];
+  const int lane = threadIdx.x & (lanes - 1), step = lanes * V::N;
+  const long long v0 =
+      ((long long)(blockIdx.x - chunks) * (kThreads / lanes) + threadIdx.x / lanes) * kRows;
+  int2 run[kRows];
+  int entry[kRows];
 #pragma unroll
-  for (int t = 0; t < V::N; ++t) a[t] = 0.f;
-#pragma unroll 4
-  for (int s = r.x; s < r.y; ++s) {
-    float f[V::N];
-    V::load(dout + (size_t)perm[s] * d + col, f);
+  for (int i = 0; i < kRows; ++i) run[i] = v0 + i < vocab ? runs[v0 + i] : make_int2(0, 0);
 #pragma unroll
-    for (int t = 0; t < V::N; ++t) a[t] += f[t];
+  for (int i = 0; i < kRows; ++i) entry[i] = run[i].x < run[i].y ? perm[run[i].x] : -1;
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    if (v0 + i >= vocab || frequent(run[i])) continue;
+    const size_t row = (size_t)(v0 + i) * d;
+    const bool one = run[i].y - run[i].x <= 1;
+    for (int col = lane * V::N; col < d; col += U * step) {
+      uint4 old[U], q[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        old[u] = q[u] = make_uint4(0, 0, 0, 0);
+        if (u == 0 || col + u * step < d) {
+          if (init) old[u] = V::raw(init + row + col + u * step);
+          if (one && entry[i] >= 0) q[u] = V::raw(dout + (size_t)entry[i] * d + col + u * step);
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (u == 0 || col + u * step < d) {
+          float a[V::N], f[V::N];
+          V::unpack(q[u], a);
+          if (!one) {
+            const T* from = dout + col + u * step;
+            for (int s = run[i].x; s < run[i].y; s += 4) {
+              uint4 x[4];
+#pragma unroll
+              for (int b = 0; b < 4; ++b)
+                x[b] = s + b < run[i].y ? V::raw(from + (size_t)perm[s + b] * d)
+                                        : make_uint4(0, 0, 0, 0);
+#pragma unroll
+              for (int b = 0; b < 4; ++b) {
+                V::unpack(x[b], f);
+#pragma unroll
+                for (int t = 0; t < V::N; ++t) a[t] += f[t];
+              }
+            }
+          }
+          V::unpack(old[u], f);
+#pragma unroll
+          for (int t = 0; t < V::N; ++t) a[t] = a[t] * scale + f[t];
+          V::store(dtable + row + col + u * step, a);
+        }
+    }
   }
-  float f[V::N];
-  V::unpack(old, f);
-#pragma unroll
-  for (int t = 0; t < V::N; ++t) a[t] = a[t] * scale + f[t];
-  V::store(dtable + (size_t)v * d + col, a);
 }
 
 template <typename T>
 cudaError_t grad_t(const TableProblem& p, const int32_t* perm, const int32_t* sorted,
                    const int2* runs, const void* dout, const void* init, void* dtable, float* part,
                    int32_t* arrived, int chunks, cudaStream_t st) {
-  int width = 1;
-  while (width < kThreads && width * Vec16<T>::N < p.d) width *= 2;
-  const long long blocks =
-      chunks + ((long long)p.vocab * (p.d / Vec16<T>::N) + kThreads - 1) / kThreads;
-  cudaError_t e = launch_dependent(embed_grad_kernel<T>, dim3((unsigned)blocks), dim3(kThreads), 0,
-                                   st, perm, sorted, runs, static_cast<const T*>(dout),
-                                   static_cast<const T*>(init), static_cast<T*>(dtable), part,
-                                   arrived, (int)p.rows, chunks, p.vocab, p.d, width, p.scale);
+  const int pieces = p.d / Vec16<T>::N, lanes = lanes_of_row(pieces);
+  int width = lanes;
+  while (width < kThreads && width < pieces) width *= 2;
+  const int each = (pieces + lanes - 1) / lanes, per_block = kThreads / lanes * kRows;
+  const long long blocks = chunks + (p.vocab + per_block - 1) / per_block;
+  auto kernel = each >= 4   ? embed_grad_kernel<T, 4>
+                : each >= 2 ? embed_grad_kernel<T, 2>
+                            : embed_grad_kernel<T, 1>;
+  cudaError_t e = launch_dependent(kernel, dim3((unsigned)blocks), dim3(kThreads), 0, st, perm, sorted,
+                                   runs, static_cast<const T*>(dout), static_cast<const T*>(init),
+                                   static_cast<T*>(dtable), part, arrived, (int)p.rows, chunks,
+                                   p.vocab, p.d, lanes, width, p.scale);
   if (e) return e;
   note_launch();
   return cudaSuccess;

@@ -39,60 +39,82 @@ route_gather_kernel(const T* __restrict__ x, const int32_t* __restrict__ undo,
   }
 }
 
-// A thread takes U pieces, kThreads apart, and B entries of each at a time:
-// all U * B loads of rows are under way before the first is used.
+// A group of `lanes` lanes (a power of two) per token: the U pieces of B
+// entries each that are under way at a time take half of the registers, which
+// is what keeps HBM busy (131 KB per SM; with the sums of all U pieces alive
+// next to them it is half of that, and 79 instead of XX us for 65536 tokens of
+// 1024 bf16, two entries each).
 template <typename T, int U, int B>
 __global__ void __launch_bounds__(kThreads)
 route_combine_kernel(const T* __restrict__ y, const float* __restrict__ weights,
                      const int32_t* __restrict__ undo, const int32_t* __restrict__ kept,
-                     T* __restrict__ out, long long pieces, int entries, int k, int d) {
+                     T* __restrict__ out, long long tokens, int entries, int k, int d, int lanes) {
   using V = Vec16<T>;
+  static_assert(U == 1 || B <= 4, "one piece where entries come in batches");
   wait_prior_grid();
-  const int per_row = d / V::N;
-  const PieceBlock at(blockIdx.x, kThreads * U, per_row);
+  const long long t = (long long)blockIdx.x * (kThreads / lanes) + threadIdx.x / lanes;
+  if (t >= tokens) return;
   const int n_kept = min(*kept, entries);
-  long long t[U];
-  int col[U];
-  float a[U][V::N];
+  const int lane = threadIdx.x & (lanes - 1), step = lanes * V::N;
+  T* to = out + (size_t)t * d;
+  int s[B];
+  float w[B];
+  // slots (-1: dropped or no such entry) and weights of entries j0..
+  auto plan = [&](int j0) {
 #pragma unroll
-  for (int u = 0; u < U; ++u) {
-    at.locate(u * kThreads + threadIdx.x, per_row, &t[u], &col[u]);
-    if (at.first + u * kThreads + threadIdx.x >= pieces) t[u] = -1;
-    col[u] *= V::N;
+    for (int j = 0; j < B; ++j) {
+      const bool in = j0 + j < k;
+      s[j] = in ? undo[t * k + j0 + j] : -1;
+      w[j] = in && weights ? weights[t * k + j0 + j] : 1.f;
+    }
 #pragma unroll
-    for (int i = 0; i < V::N; ++i) a[u][i] = 0.f;
-  }
-  for (int j0 = 0; j0 < k; j0 += B) {
-    int s[U][B];
-    float w[U][B];
+    for (int j = 0; j < B; ++j)
+      if (s[j] >= n_kept) s[j] = -1;
+  };
+  plan(0);
+  for (int col = lane * V::N; col < d; col += U * step) {
     uint4 v[U][B];
+    auto load = [&] {
 #pragma unroll
-    for (int u = 0; u < U; ++u)
+      for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int j = 0; j < B; ++j) {
-        const bool in = t[u] >= 0 && j0 + j < k;
-        s[u][j] = in ? undo[t[u] * k + j0 + j] : -1;
-        w[u][j] = in && weights ? weights[t[u] * k + j0 + j] : 1.f;
-      }
-#pragma unroll
-    for (int u = 0; u < U; ++u)
-#pragma unroll
-      for (int j = 0; j < B; ++j)
-        if (s[u][j] >= 0 && s[u][j] < n_kept) v[u][j] = V::raw(y + (size_t)s[u][j] * d + col[u]);
-#pragma unroll
-    for (int u = 0; u < U; ++u)
+        for (int j = 0; j < B; ++j)
+          if (s[j] >= 0 && (u == 0 || col + u * step < d))
+            v[u][j] = V::raw(y + (size_t)s[j] * d + col + u * step);
+    };
+    auto add = [&](int u, float* a) {
 #pragma unroll
       for (int j = 0; j < B; ++j)
-        if (s[u][j] >= 0 && s[u][j] < n_kept) {
+        if (s[j] >= 0) {
           float f[V::N];
           V::unpack(v[u][j], f);
 #pragma unroll
-          for (int i = 0; i < V::N; ++i) a[u][i] = fmaf(w[u][j], f[i], a[u][i]);
+          for (int i = 0; i < V::N; ++i) a[i] = fmaf(w[j], f[i], a[i]);
         }
-  }
+    };
+    if constexpr (B <= 4) {  // k <= B
+      load();
 #pragma unroll
-  for (int u = 0; u < U; ++u)
-    if (t[u] >= 0) V::store(out + (size_t)t[u] * d + col[u], a[u]);
+      for (int u = 0; u < U; ++u)
+        if (u == 0 || col + u * step < d) {
+          float a[V::N];
+#pragma unroll
+          for (int i = 0; i < V::N; ++i) a[i] = 0.f;
+          add(u, a);
+          V::store(to + col + u * step, a);
+        }
+    } else {
+      float a[V::N];
+#pragma unroll
+      for (int i = 0; i < V::N; ++i) a[i] = 0.f;
+      for (int j0 = 0; j0 < k; j0 += B) {
+        if (k > B) plan(j0);
+        load();
+        add(0, a);
+      }
+      V::store(to + col, a);
+    }
+  }
 }
 
 // A group of `lanes` lanes (a power of two) per token, kBatch entries at a
@@ -171,14 +193,29 @@ cudaError_t gather_t(const RouteProblem& p, const void* x, const int32_t* undo,
                           (int)p.entries(), p.k, p.d);
 }
 
+template <typename T, int U, int B>
+cudaError_t combine_ub(const RouteProblem& p, const void* y, const float* weights,
+                       const int32_t* undo, const int32_t* kept, void* out, int lanes,
+                       cudaStream_t st) {
+  return launch_dependent(route_combine_kernel<T, U, B>, dim3(blocks_of(p.tokens * lanes)),
+                          dim3(kThreads), 0, st, static_cast<const T*>(y), weights, undo, kept,
+                          static_cast<T*>(out), p.tokens, (int)p.entries(), p.k, p.d, lanes);
+}
+
+// Eight loads under way per thread where a row is that long.
 template <typename T>
 cudaError_t combine_t(const RouteProblem& p, const void* y, const float* weights,
                       const int32_t* undo, const int32_t* kept, void* out, cudaStream_t st) {
-  const long long pieces = p.tokens * (p.d / Vec16<T>::N);
-  auto kernel = p.k <= 2 ? route_combine_kernel<T, 2, 2> : route_combine_kernel<T, 1, 4>;
-  return launch_dependent(kernel, dim3(blocks_of(p.k <= 2 ? (pieces + 1) / 2 : pieces)),
-                          dim3(kThreads), 0, st, static_cast<const T*>(y), weights, undo, kept,
-                          static_cast<T*>(out), pieces, (int)p.entries(), p.k, p.d);
+  const int pieces = p.d / Vec16<T>::N, lanes = lanes_of_row(pieces);
+  const int each = (pieces + lanes - 1) / lanes;
+  if (p.k <= 2)
+    return each >= 4   ? combine_ub<T, 4, 2>(p, y, weights, undo, kept, out, lanes, st)
+           : each >= 2 ? combine_ub<T, 2, 2>(p, y, weights, undo, kept, out, lanes, st)
+                       : combine_ub<T, 1, 2>(p, y, weights, undo, kept, out, lanes, st);
+  if (p.k <= 4)
+    return each >= 2 ? combine_ub<T, 2, 4>(p, y, weights, undo, kept, out, lanes, st)
+                     : combine_ub<T, 1, 4>(p, y, weights, undo, kept, out, lanes, st);
+  return combine_ub<T, 1, 8>(p, y, weights, undo, kept, out, lanes, st);
 }
 
 template <typename T>
