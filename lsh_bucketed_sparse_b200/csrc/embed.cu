@@ -6,12 +6,10 @@
 // Lookup: a copy of 16-byte pieces, bound by memory.
 //
 // Gradient: the tokens are ordered by id (key_sort.cu), so a table row's sum
-// runs over consecutive slots and is written once, without atomics: the sum's
-// order is fixed by the input alone.  Sums are float32 and rounded once.  A
-// run of up to kChunk slots is summed by the threads that own the row's
-// pieces.  Longer runs (frequent tokens) are cut at multiples of kChunk: one
-// CTA per chunk leaves a float32 partial sum, and the last of a run's CTAs to
-// finish adds them in order.
+// runs over consecutive slots and is written once: the sum's order is fixed
+// by the input alone.  Sums are float32 and rounded once.  The work is cut
+// over slots, not over table rows, so that frequent tokens cost no more than
+// rare ones; runs that cross a cut are joined in their order.
 #include "common.cuh"
 #include "internal.h"
 #include "vec16.cuh"
@@ -20,7 +18,8 @@ namespace lsh {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kChunk = 64;  // longest run summed in one go
+constexpr int kWindow = 32;   // slots that a group of lanes adds up
+constexpr int kMinLanes = 8;  // of a group
 
 // A thread takes kPieces pieces, kThreads apart: its tokens, then its rows are
 // under way together.
@@ -62,188 +61,219 @@ embed_kernel(const I* __restrict__ tokens, const T* __restrict__ table, T* __res
   }
 }
 
-__device__ __forceinline__ bool frequent(int2 run) { return run.y - run.x > kChunk; }
-
-// Threads that share a row of float32 partial sums, four columns each.
-__device__ __forceinline__ int width4(int width, int d) {
-  while (width < kThreads && width * 4 < d) width *= 2;
-  return width;
+// out[.. V::N values] = a * scale (+ init).
+template <typename T>
+__device__ __forceinline__ void put_row(T* out, const float* a, float scale, bool add,
+                                        const uint4& old) {
+  using V = Vec16<T>;
+  float f[V::N];
+  V::unpack(old, f);
+#pragma unroll
+  for (int t = 0; t < V::N; ++t) f[t] = add ? fmaf(a[t], scale, f[t]) : a[t] * scale;
+  V::store(out, f);
 }
 
-// Sum of `count` rows of `d` values, row i at src(i), over the block:
-// `width` threads (a power of two) share a row, the block's kThreads / width
-// groups share the rows, and the groups' sums are added in order.  The block's
-// first `width` threads get the values; emit(col, values) is called for their
-// columns.
-template <int N, typename Load, typename Emit>
-__device__ void block_sum_rows(int count, int d, int width, float* sums, Load load, Emit emit) {
-  const int groups = kThreads / width, grp = threadIdx.x / width, at = threadIdx.x & (width - 1);
-  for (int col0 = 0; col0 < d; col0 += width * N) {
-    const int col = col0 + at * N;
-    float a[N];
-#pragma unroll
-    for (int t = 0; t < N; ++t) a[t] = 0.f;
-    if (col < d) {
-#pragma unroll 8
-      for (int s = grp; s < count; s += groups) {
-        float f[N];
-        load(s, col, f);
-#pragma unroll
-        for (int t = 0; t < N; ++t) a[t] += f[t];
-      }
-    }
-    if (groups > 1) {
-#pragma unroll
-      for (int t = 0; t < N; ++t) sums[t * kThreads + threadIdx.x] = a[t];
-      __syncthreads();
-      if (grp == 0)
-        for (int o = 1; o < groups; ++o)
-#pragma unroll
-          for (int t = 0; t < N; ++t) a[t] += sums[t * kThreads + o * width + at];
-      __syncthreads();
-    }
-    if (grp == 0 && col < d) emit(col, a);
-  }
-}
-
-// Blocks [0, chunks): the chunk's partial sums of frequent tokens, at most
-// two (the run of its first slot -> part[chunk][0], another run that reaches
-// past its end -> part[chunk][1]).  The block that completes a run's partial
-// sums (arrived[], counted at the run's first chunk) adds them in their order
-// and writes the table's row.  Later blocks: kRows table rows per group of
-// `lanes` lanes (a power of two), for rows that are not frequent: the runs and
-// first entries of all of them are read at once; U pieces of a row are under
-// way at a time where it has one entry at most, four entries of a piece where
-// it has more.
-constexpr int kRows = 4;
-template <typename T, int U>
-__global__ void __launch_bounds__(kThreads)
+// Blocks [0, slot_blocks * col_blocks): a block takes kThreads / lanes windows
+// of kWindow consecutive slots and `lanes` 16-byte pieces of every row; a
+// group of `lanes` lanes adds up the rows of one window, whose loads depend
+// on nothing but the plan in shared memory.  A run inside a window is written
+// at once.  Runs that cross windows are joined in shared memory, in order, by
+// the block's first group; what crosses blocks goes to part[block][0] (the run
+// of the block's first slot) or [1], and the block that completes a run
+// (arrived[], counted at its first block) adds its partial sums in order.
+// Later blocks: table rows without a token.
+// Rows under way per thread and resident blocks, measured on 65536 x 1024 bf16
+// tokens without and 12287 x 520 float32 tokens with init: 4 rows, 4 blocks
+// 54.0 / -, 6 and 4 49.5 us / -, 8 and 3 54.5 us; with init 4 and 4 53.6 us,
+// 2 and 5 48.2, 2 and 6 44.7 (bf16 has no registers for a sixth block).
+template <typename T, bool kInit>
+__global__ void __launch_bounds__(kThreads, !kInit ? 4 : sizeof(T) == 4 ? 6 : 5)
 embed_grad_kernel(const int32_t* __restrict__ perm, const int32_t* __restrict__ sorted,
                   const int2* __restrict__ runs, const T* __restrict__ dout, const T* init,
-                  T* dtable, float* part, int32_t* arrived, int n, int chunks, int vocab, int d,
-                  int lanes, int width, float scale) {
+                  T* dtable, float* part, int32_t* arrived, int n, int slot_blocks, int col_blocks,
+                  int vocab, int d, int lanes, float scale) {
   using V = Vec16<T>;
+  constexpr int kAhead = kInit ? 2 : 6;
+  const int max_slots = kThreads / kMinLanes * kWindow;
+  __shared__ int32_t keys_mem[max_slots + 2], entry[max_slots];
+  __shared__ float sums[2 * kThreads * V::N];
+  __shared__ int32_t open_key[2 * (kThreads / kMinLanes)];
   wait_prior_grid();
-  if ((int)blockIdx.x < chunks) {
-    __shared__ int32_t rows[kChunk];
-    __shared__ float sums[kThreads * V::N];
-    __shared__ int last;
-    const int c0 = blockIdx.x * kChunk, c1 = min(n, c0 + kChunk);
-    const int k0 = sorted[c0], k1 = sorted[c1 - 1];
-    const int2 r0 = k0 < vocab ? runs[k0] : make_int2(0, 0);
-    const int2 r1 = k1 < vocab && k1 != k0 ? runs[k1] : make_int2(0, 0);
-    if (!frequent(r0) && !frequent(r1)) return;
-    for (int s = c0 + threadIdx.x; s < c1; s += kThreads) rows[s - c0] = perm[s];
-    __syncthreads();
-    for (int which = 0; which < 2; ++which) {
-      const int2 r = which ? r1 : r0;
-      if (!frequent(r)) continue;
-      const int b = max(r.x, c0) - c0, e = min(r.y, c1) - c0;
-      float* to = part + ((size_t)blockIdx.x * 2 + which) * d;
-      block_sum_rows<V::N>(
-          e - b, d, width, sums,
-          [&](int s, int col, float* f) { V::load(dout + (size_t)rows[b + s] * d + col, f); },
-          [&](int col, const float* a) {
+  if ((int)blockIdx.x >= slot_blocks * col_blocks) {
+    const int per_row = d / V::N;
+    const PieceBlock at(blockIdx.x - slot_blocks * col_blocks, kThreads * kPieces, per_row);
+    int2 run[kPieces];
+    const long long pieces = (long long)vocab * per_row;
 #pragma unroll
-            for (int t = 0; t < V::N; t += 4)
-              *reinterpret_cast<float4*>(to + col + t) =
-                  make_float4(a[t], a[t + 1], a[t + 2], a[t + 3]);
-          });
-      const int first = r.x / kChunk, count = (r.y - 1) / kChunk - first + 1;
-      __threadfence();
-      __syncthreads();
-      if (threadIdx.x == 0) last = atomicAdd(&arrived[first], 1) == count - 1;
-      __syncthreads();
-      if (!last) continue;
-      __threadfence();
-      const size_t row = (size_t)(which ? k1 : k0) * d;
-      const bool shared = r.x > first * kChunk;  // the first chunk begins with another run
-      block_sum_rows<4>(
-          count, d, width4(width, d), sums,
-          [&](int c, int col, float* f) {
-            const size_t at = ((size_t)(first + c) * 2 + (c == 0 && shared)) * d + col;
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(part + at));
-            f[0] = x.x; f[1] = x.y; f[2] = x.z; f[3] = x.w;
-          },
-          [&](int col, const float* a) {
+    for (int u = 0; u < kPieces; ++u) {
+      long long v;
+      int col;
+      at.locate(u * kThreads + threadIdx.x, per_row, &v, &col);
+      run[u] = v < vocab ? runs[v] : make_int2(0, 1);
+    }
 #pragma unroll
-            for (int t = 0; t < 4; ++t)
-              dtable[row + col + t] =
-                  from_f32<T>(a[t] * scale + (init ? to_f32(init[row + col + t]) : 0.f));
-          });
+    for (int u = 0; u < kPieces; ++u) {
+      const long long p = at.first + u * kThreads + threadIdx.x;
+      if (p >= pieces || run[u].x != run[u].y) continue;
+      uint4 old = make_uint4(0, 0, 0, 0);
+      if (kInit) old = V::raw(init + p * V::N);
+      *reinterpret_cast<uint4*>(dtable + p * V::N) = old;
     }
     return;
   }
-  const int lane = threadIdx.x & (lanes - 1), step = lanes * V::N;
-  const long long v0 =
-      ((long long)(blockIdx.x - chunks) * (kThreads / lanes) + threadIdx.x / lanes) * kRows;
-  int2 run[kRows];
-  int entry[kRows];
+  const int sb = blockIdx.x / col_blocks, cb = blockIdx.x - sb * col_blocks;
+  const int groups = kThreads / lanes, grp = threadIdx.x / lanes, lane = threadIdx.x & (lanes - 1);
+  const int per_block = groups * kWindow;
+  const int b0 = sb * per_block, b1 = min(n, b0 + per_block);
+  const int32_t* keys = keys_mem + 1 - b0;  // keys[b0 - 1 .. b1], -1 outside [0, n)
+  const int32_t* ent = entry - b0;
+  for (int i = threadIdx.x; i < b1 - b0 + 2; i += kThreads) {
+    const int s = b0 - 1 + i;
+    keys_mem[i] = s >= 0 && s < n ? sorted[s] : -1;
+  }
+  for (int i = threadIdx.x; i < b1 - b0; i += kThreads) entry[i] = perm[b0 + i];
+  if (threadIdx.x < 2 * groups) open_key[threadIdx.x] = -1;
+  __syncthreads();
+  const int col = (cb * lanes + lane) * V::N;
+  const bool live = col < d;
+  const int g0 = b0 + grp * kWindow, g1 = min(b1, g0 + kWindow);
+  if (g0 < g1) {
+    bool open_left = keys[g0 - 1] == keys[g0];
+    float a[V::N];
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) run[i] = v0 + i < vocab ? runs[v0 + i] : make_int2(0, 0);
+    for (int t = 0; t < V::N; ++t) a[t] = 0.f;
+    for (int s0 = g0; s0 < g1; s0 += kAhead) {
+      uint4 x[kAhead], old[kInit ? kAhead : 1];
+      old[0] = make_uint4(0, 0, 0, 0);
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) entry[i] = run[i].x < run[i].y ? perm[run[i].x] : -1;
-#pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    if (v0 + i >= vocab || frequent(run[i])) continue;
-    const size_t row = (size_t)(v0 + i) * d;
-    const bool one = run[i].y - run[i].x <= 1;
-    for (int col = lane * V::N; col < d; col += U * step) {
-      uint4 old[U], q[U];
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        old[u] = q[u] = make_uint4(0, 0, 0, 0);
-        if (u == 0 || col + u * step < d) {
-          if (init) old[u] = V::raw(init + row + col + u * step);
-          if (one && entry[i] >= 0) q[u] = V::raw(dout + (size_t)entry[i] * d + col + u * step);
+      for (int i = 0; i < kAhead; ++i) {
+        const int s = s0 + i;
+        const bool on = live && s < g1 && keys[s] < vocab;
+        x[i] = make_uint4(0, 0, 0, 0);
+        if (on) x[i] = V::raw(dout + (size_t)ent[s] * d + col);
+        if constexpr (kInit) {
+          if (on && keys[s + 1] != keys[s]) old[i] = V::raw(init + (size_t)keys[s] * d + col);
         }
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (u == 0 || col + u * step < d) {
-          float a[V::N], f[V::N];
-          V::unpack(q[u], a);
-          if (!one) {
-            const T* from = dout + col + u * step;
-            for (int s = run[i].x; s < run[i].y; s += 4) {
-              uint4 x[4];
+      for (int i = 0; i < kAhead; ++i) {
+        const int s = s0 + i;
+        if (s >= g1) continue;
+        const int k = keys[s];
+        float f[V::N];
+        V::unpack(x[i], f);
 #pragma unroll
-              for (int b = 0; b < 4; ++b)
-                x[b] = s + b < run[i].y ? V::raw(from + (size_t)perm[s + b] * d)
-                                        : make_uint4(0, 0, 0, 0);
+        for (int t = 0; t < V::N; ++t) a[t] += f[t];
+        const bool ends = keys[s + 1] != k;
+        if (!ends && s + 1 < g1) continue;
+        if (k < vocab && live) {
+          if (ends && !open_left) {
+            put_row(dtable + (size_t)k * d + col, a, scale, kInit, old[kInit ? i : 0]);
+          } else {
+            const int slot = 2 * grp + (open_left ? 0 : 1);
+            if (lane == 0) open_key[slot] = k;
 #pragma unroll
-              for (int b = 0; b < 4; ++b) {
-                V::unpack(x[b], f);
+            for (int t = 0; t < V::N; ++t) sums[(slot * V::N + t) * lanes + lane] = a[t];
+          }
+        }
+        open_left = false;
 #pragma unroll
-                for (int t = 0; t < V::N; ++t) a[t] += f[t];
+        for (int t = 0; t < V::N; ++t) a[t] = 0.f;
+      }
+    }
+  }
+  __syncthreads();
+  if (grp != 0) return;
+  const unsigned mask = (lanes == 32 ? 0u : 1u << lanes) - 1u;  // lanes of the first group
+  int cur = -1;
+  float a[V::N];
+#pragma unroll
+  for (int t = 0; t < V::N; ++t) a[t] = 0.f;
+  for (int q = 0; q <= 2 * groups; ++q) {
+    const int k = q < 2 * groups ? open_key[q] : -1;
+    if (q < 2 * groups && k < 0) continue;
+    if (k != cur && cur >= 0) {
+      // the run of cur is complete as far as this block goes
+      const bool left = keys[b0] == cur && keys[b0 - 1] == cur;
+      const bool right = keys[b1 - 1] == cur && keys[b1] == cur;
+      const size_t row = (size_t)cur * d + col;
+      bool write = !left && !right;
+      if (!write) {
+        float* to = part + ((size_t)sb * 2 + (keys[b0] == cur ? 0 : 1)) * d + col;
+        if (live) {
+#pragma unroll
+          for (int t = 0; t < V::N; t += 4)
+            *reinterpret_cast<float4*>(to + t) = make_float4(a[t], a[t + 1], a[t + 2], a[t + 3]);
+        }
+        const int2 r = runs[cur];
+        const int first = r.x / per_block, count = (r.y - 1) / per_block - first + 1;
+        __threadfence();
+        __syncwarp(mask);
+        int before = 0;
+        if (lane == 0) before = atomicAdd(&arrived[first * col_blocks + cb], 1);
+        before = __shfl_sync(mask, before, 0);
+        if (before == count - 1) {
+          __threadfence();
+          write = true;
+          const bool shared = r.x > first * per_block;  // its first block begins with another run
+#pragma unroll
+          for (int t = 0; t < V::N; ++t) a[t] = 0.f;
+          if (live) {
+#pragma unroll 4
+            for (int c = 0; c < count; ++c) {
+              const float* from = part + ((size_t)(first + c) * 2 + (c == 0 && shared)) * d + col;
+#pragma unroll
+              for (int t = 0; t < V::N; t += 4) {
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(from + t));
+                a[t] += v.x; a[t + 1] += v.y; a[t + 2] += v.z; a[t + 3] += v.w;
               }
             }
           }
-          V::unpack(old[u], f);
-#pragma unroll
-          for (int t = 0; t < V::N; ++t) a[t] = a[t] * scale + f[t];
-          V::store(dtable + row + col + u * step, a);
         }
+      }
+      if (write && live)
+        put_row(dtable + row, a, scale, kInit,
+                kInit ? V::raw(init + row) : make_uint4(0, 0, 0, 0));
+#pragma unroll
+      for (int t = 0; t < V::N; ++t) a[t] = 0.f;
+    }
+    cur = k;
+    if (k >= 0) {
+#pragma unroll
+      for (int t = 0; t < V::N; ++t) a[t] += sums[(q * V::N + t) * lanes + lane];
     }
   }
+}
+
+// How the gradient's blocks cut slots and columns.
+struct Cut {
+  int lanes, slots, slot_blocks, col_blocks;
+};
+
+Cut cut_of(const TableProblem& p) {
+  const int pieces = (int)(p.d * p.elem() / 16);
+  Cut c;
+  c.lanes = lanes_of_row(pieces);
+  if (c.lanes < kMinLanes) c.lanes = kMinLanes;
+  c.slots = kThreads / c.lanes * kWindow;
+  c.slot_blocks = (int)((p.rows + c.slots - 1) / c.slots);
+  c.col_blocks = (pieces + c.lanes - 1) / c.lanes;
+  return c;
 }
 
 template <typename T>
 cudaError_t grad_t(const TableProblem& p, const int32_t* perm, const int32_t* sorted,
                    const int2* runs, const void* dout, const void* init, void* dtable, float* part,
-                   int32_t* arrived, int chunks, cudaStream_t st) {
-  const int pieces = p.d / Vec16<T>::N, lanes = lanes_of_row(pieces);
-  int width = lanes;
-  while (width < kThreads && width < pieces) width *= 2;
-  const int each = (pieces + lanes - 1) / lanes, per_block = kThreads / lanes * kRows;
-  const long long blocks = chunks + (p.vocab + per_block - 1) / per_block;
-  auto kernel = each >= 4   ? embed_grad_kernel<T, 4>
-                : each >= 2 ? embed_grad_kernel<T, 2>
-                            : embed_grad_kernel<T, 1>;
-  cudaError_t e = launch_dependent(kernel, dim3((unsigned)blocks), dim3(kThreads), 0, st, perm, sorted,
+                   int32_t* arrived, const Cut& c, cudaStream_t st) {
+  // rows without a token: nothing to do where the gradient is added in place
+  const long long pieces = init == dtable ? 0 : (long long)p.vocab * (p.d / Vec16<T>::N);
+  const long long blocks = (long long)c.slot_blocks * c.col_blocks +
+                           (pieces + kThreads * kPieces - 1) / (kThreads * kPieces);
+  cudaError_t e = launch_dependent(init ? embed_grad_kernel<T, true> : embed_grad_kernel<T, false>,
+                                   dim3((unsigned)blocks), dim3(kThreads), 0, st, perm, sorted,
                                    runs, static_cast<const T*>(dout), static_cast<const T*>(init),
-                                   static_cast<T*>(dtable), part, arrived, (int)p.rows, chunks,
-                                   p.vocab, p.d, lanes, width, p.scale);
+                                   static_cast<T*>(dtable), part, arrived, (int)p.rows,
+                                   c.slot_blocks, c.col_blocks, p.vocab, p.d, c.lanes, p.scale);
   if (e) return e;
   note_launch();
   return cudaSuccess;
@@ -292,21 +322,24 @@ cudaError_t embed_t(const TableProblem& p, const void* tokens, const void* table
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 struct Scratch {
-  int chunks;  // none where no run can be that long
   size_t perm, sorted, runs, part, arrived, sort, total;
+  int n_arrived;  // counters, none where one block takes all slots
 };
 
 Scratch scratch_layout(const TableProblem& p) {
   const size_t n = (size_t)p.rows;
+  const Cut c = cut_of(p);
+  const bool joins = c.slot_blocks > 1;
   Scratch s;
   size_t off = 0;
-  s.perm = off;   off += align256(n * sizeof(int32_t));
-  s.sorted = off; off += align256(n * sizeof(int32_t));
-  s.runs = off;   off += align256((size_t)p.vocab * sizeof(int2));
-  s.chunks = p.rows > kChunk ? (int)((n + kChunk - 1) / kChunk) : 0;
-  s.part = off;   off += align256((size_t)s.chunks * 2 * p.d * sizeof(float));
-  s.arrived = off; off += align256((size_t)s.chunks * sizeof(int32_t));
-  s.sort = off;   off += key_sort_scratch_bytes(p.rows, p.vocab);
+  // (at most n: a block of slots has at least 256, a row at most 128 column blocks)
+  s.n_arrived = joins ? c.slot_blocks * c.col_blocks : 0;
+  s.perm = off;    off += align256(n * sizeof(int32_t));
+  s.sorted = off;  off += align256(n * sizeof(int32_t));
+  s.runs = off;    off += align256((size_t)p.vocab * sizeof(int2));
+  s.part = off;    off += joins ? align256((size_t)c.slot_blocks * 2 * p.d * sizeof(float)) : 0;
+  s.arrived = off; off += align256((size_t)s.n_arrived * sizeof(int32_t));
+  s.sort = off;    off += key_sort_scratch_bytes(p.rows, p.vocab);
   s.total = off;
   return s;
 }
@@ -342,12 +375,12 @@ cudaError_t launch_embed_backward(const TableProblem& p, const void* tokens, con
   float* part = reinterpret_cast<float*>(base + s.part);
   int32_t* arrived = reinterpret_cast<int32_t*>(base + s.arrived);
   cudaError_t e = launch_key_sort(p.rows, p.vocab, tokens, p.idx64, perm, nullptr, nullptr, sorted,
-                                  runs, arrived, s.chunks, base + s.sort, st);
+                                  runs, arrived, s.n_arrived, base + s.sort, st);
   if (e) return e;
-  return p.bf16 ? grad_t<__nv_bfloat16>(p, perm, sorted, runs, dout, init, dtable, part, arrived,
-                                        s.chunks, st)
-                : grad_t<float>(p, perm, sorted, runs, dout, init, dtable, part, arrived, s.chunks,
-                                st);
+  const Cut c = cut_of(p);
+  return p.bf16 ? grad_t<__nv_bfloat16>(p, perm, sorted, runs, dout, init, dtable, part, arrived, c,
+                                        st)
+                : grad_t<float>(p, perm, sorted, runs, dout, init, dtable, part, arrived, c, st);
 }
 
 }  // namespace lsh

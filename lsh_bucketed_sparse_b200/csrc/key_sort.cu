@@ -5,7 +5,7 @@
 // The key K included, keys have nbits = bits(K) bits.  Up to kOneDigitBits
 // they are one digit and one stable counting pass orders them; above that
 // the low and the high half of the bits are two digits, one pass each.  A
-// pass cuts the entries into tiles of kTile:
+// pass cuts the entries into tiles:
 //   count    one CTA per tile: its entries per digit value;
 //   scan     one CTA: per digit value the exclusive sum over the tiles, then
 //            the first slot of every value (their exclusive sum); up to
@@ -21,18 +21,17 @@
 namespace lsh {
 namespace {
 
-constexpr int kTile = 2048;
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
-constexpr int kPer = kTile / kThreads;      // entries per thread
 constexpr int kScanThreads = 1024;
 constexpr int kOneDigitBits = 10;
 constexpr int kMaxBins = 1 << 11;
 constexpr int kFusedTiles = 64;
+constexpr int kSmallPer = 4, kLargePer = 8;  // entries per thread
 
 struct Plan {
   int bits, lo, hi;  // hi == 0: one digit of `lo` = `bits` bits
-  int tiles;
+  int per, tiles;    // entries per thread, tiles of kThreads * per entries
   int bins_lo, bins_hi;
 };
 
@@ -50,7 +49,13 @@ Plan make_plan(long long n, int K) {
     p.bins_lo = 1 << p.lo;
     p.bins_hi = (K >> p.lo) + 1;
   }
-  p.tiles = (int)((n + kTile - 1) / kTile);
+  // one tile while one holds them all, small tiles while the scatter's CTAs can
+  // add up their counts themselves (both passes and the runs of 12287 tokens
+  // over 50021 words: 17.1 us in tiles of 1024, 21.5 of 2048; 65536 tokens over
+  // 32768: 22.0 and 22.3)
+  const int small = kThreads * kSmallPer, large = kThreads * kLargePer;
+  p.per = n > large && n <= (long long)small * kFusedTiles ? kSmallPer : kLargePer;
+  p.tiles = (int)((n + kThreads * p.per - 1) / (kThreads * p.per));
   return p;
 }
 
@@ -74,7 +79,7 @@ struct OrderedKeys {
   __device__ int entry(int e) const { return entries[e]; }
 };
 
-template <typename S>
+template <typename S, int kPer>
 __global__ void __launch_bounds__(kThreads)
 key_count_kernel(const S src, int32_t* __restrict__ cnt, int2* __restrict__ runs, int n_runs,
                  int n, int bins, int shift, int mask) {
@@ -82,7 +87,7 @@ key_count_kernel(const S src, int32_t* __restrict__ cnt, int2* __restrict__ runs
   for (int b = threadIdx.x; b < bins; b += kThreads) hist[b] = 0;
   wait_prior_grid();
   __syncthreads();
-  const int beg = blockIdx.x * kTile;
+  const int beg = blockIdx.x * (kThreads * kPer);
   int dg[kPer];
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
@@ -172,24 +177,23 @@ key_scan_kernel(int32_t* __restrict__ cnt, int32_t* __restrict__ base_out,
 // kScanned: cnt and base come from the scan kernel.  Otherwise cnt holds the
 // tiles' plain counts (not read when there is one tile) and every CTA adds up
 // for itself what stands before it.
-template <typename S, bool kScanned>
+template <typename S, int kPer, bool kScanned>
 __global__ void __launch_bounds__(kThreads)
 key_scatter_kernel(const S src, const int32_t* __restrict__ cnt, const int32_t* __restrict__ base,
                    int32_t* __restrict__ perm, int32_t* __restrict__ undo,
                    int32_t* __restrict__ sorted, int32_t* __restrict__ offsets,
-                   int2* __restrict__ runs, int n_runs, int n, int tiles, int bins, int bits,
-                   int shift, int mask) {
+                   int2* __restrict__ runs, int n_runs, int n, int tiles, int bins, int shift,
+                   int mask) {
   extern __shared__ int32_t off[];  // [kWarps][bins], then without kScanned first[bins], before[bins]
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int32_t* mine = off + (size_t)warp * bins;
   for (int b = lane; b < bins; b += 32) mine[b] = 0;
   wait_prior_grid();
-  constexpr int kRows = kTile / kWarps / 32;
-  const int beg = blockIdx.x * kTile + warp * (kTile / kWarps);
-  int key[kRows], entry[kRows];
-  unsigned peers[kRows];
+  const int beg = (blockIdx.x * kWarps + warp) * (32 * kPer);
+  int key[kPer], entry[kPer];
+  unsigned peers[kPer];
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) {
+  for (int i = 0; i < kPer; ++i) {
     const int e = beg + 32 * i + lane;
     key[i] = e < n ? src.key(e) : -1;
     entry[i] = e < n ? src.entry(e) : 0;
@@ -199,16 +203,10 @@ key_scatter_kernel(const S src, const int32_t* __restrict__ cnt, const int32_t* 
     runs[v] = make_int2(0, 0);
   __syncwarp();
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) {
+  for (int i = 0; i < kPer; ++i) {
     const bool valid = key[i] >= 0;
     const int dg = (key[i] >> shift) & mask;
-    const unsigned v = __ballot_sync(0xffffffffu, valid);
-    unsigned m = valid ? v : 0;
-    for (int k = 0; k < bits; ++k) {
-      const bool bit = (dg >> k) & 1;
-      const unsigned x = __ballot_sync(0xffffffffu, valid && bit);
-      m &= bit ? x : ~x;
-    }
+    const unsigned m = __match_any_sync(0xffffffffu, valid ? dg : -1);
     peers[i] = m;
     if (valid && lane == 31 - __clz(m)) mine[dg] += __popc(m);
     __syncwarp();
@@ -256,7 +254,7 @@ key_scatter_kernel(const S src, const int32_t* __restrict__ cnt, const int32_t* 
   }
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) {
+  for (int i = 0; i < kPer; ++i) {
     const bool valid = key[i] >= 0;
     const int dg = (key[i] >> shift) & mask;
     int slot = 0;
@@ -306,8 +304,8 @@ Scratch scratch_layout(long long n, const Plan& p) {
   return s;
 }
 
-template <typename S>
-cudaError_t one_pass(const S& src, int32_t* cnt, int32_t* base, int32_t* offsets, int32_t* perm,
+template <typename S, int kPer>
+cudaError_t one_pass_per(const S& src, int32_t* cnt, int32_t* base, int32_t* offsets, int32_t* perm,
                      int32_t* undo, int32_t* sorted, int2* runs, int n_runs, int n, int tiles,
                      int bins, int bits, int shift, cudaStream_t st) {
   const int mask = (1 << bits) - 1;
@@ -315,7 +313,7 @@ cudaError_t one_pass(const S& src, int32_t* cnt, int32_t* base, int32_t* offsets
   const bool fused = tiles <= kFusedTiles;
   cudaError_t e;
   if (tiles > 1) {
-    if ((e = launch_dependent(key_count_kernel<S>, dim3(tiles), dim3(kThreads), row, st, src, cnt,
+    if ((e = launch_dependent(key_count_kernel<S, kPer>, dim3(tiles), dim3(kThreads), row, st, src, cnt,
                               runs, n_runs, n, bins, shift, mask)))
       return e;
     note_launch();
@@ -327,18 +325,28 @@ cudaError_t one_pass(const S& src, int32_t* cnt, int32_t* base, int32_t* offsets
       return e;
     note_launch();
   }
-  auto kernel = fused ? key_scatter_kernel<S, false> : key_scatter_kernel<S, true>;
+  auto kernel = fused ? key_scatter_kernel<S, kPer, false> : key_scatter_kernel<S, kPer, true>;
   const size_t smem = (kWarps + (fused ? 2 : 0)) * row;
   if (smem > 48 * 1024 &&
       (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)))
     return e;
   if ((e = launch_dependent(kernel, dim3(tiles), dim3(kThreads), smem, st, src,
                             static_cast<const int32_t*>(cnt), static_cast<const int32_t*>(base),
-                            perm, undo, sorted, offsets, runs, n_runs, n, tiles, bins, bits, shift,
-                            mask)))
+                            perm, undo, sorted, offsets, runs, n_runs, n, tiles, bins, shift, mask)))
     return e;
   note_launch();
   return cudaSuccess;
+}
+
+template <typename S>
+cudaError_t one_pass(const Plan& p, const S& src, int32_t* cnt, int32_t* base, int32_t* offsets,
+                     int32_t* perm, int32_t* undo, int32_t* sorted, int2* runs, int n_runs, int n,
+                     int bins, int bits, int shift, cudaStream_t st) {
+  return p.per == kSmallPer
+             ? one_pass_per<S, kSmallPer>(src, cnt, base, offsets, perm, undo, sorted, runs, n_runs,
+                                          n, p.tiles, bins, bits, shift, st)
+             : one_pass_per<S, kLargePer>(src, cnt, base, offsets, perm, undo, sorted, runs, n_runs,
+                                          n, p.tiles, bins, bits, shift, st);
 }
 
 }  // namespace
@@ -366,15 +374,15 @@ cudaError_t launch_key_sort(long long n_, int K, const void* keys, bool keys64, 
   int32_t* to_perm = p.hi ? e1 : perm;
   int32_t* to_undo = p.hi ? nullptr : undo;
   int32_t* to_sorted = p.hi ? k1 : sorted;
-  cudaError_t e = keys64 ? one_pass(r64, cnt, first, offsets, to_perm, to_undo, to_sorted, runs,
-                                    n_runs, n, p.tiles, p.bins_lo, p.lo, 0, st)
-                         : one_pass(r32, cnt, first, offsets, to_perm, to_undo, to_sorted, runs,
-                                    n_runs, n, p.tiles, p.bins_lo, p.lo, 0, st);
+  cudaError_t e = keys64 ? one_pass(p, r64, cnt, first, offsets, to_perm, to_undo, to_sorted,
+                                    runs, n_runs, n, p.bins_lo, p.lo, 0, st)
+                         : one_pass(p, r32, cnt, first, offsets, to_perm, to_undo, to_sorted,
+                                    runs, n_runs, n, p.bins_lo, p.lo, 0, st);
   if (e) return e;
   if (p.hi) {
     const OrderedKeys ord{k1, e1};
-    if ((e = one_pass(ord, cnt, first, nullptr, perm, undo, sorted, nullptr, 0, n, p.tiles,
-                      p.bins_hi, p.hi, p.lo, st)))
+    if ((e = one_pass(p, ord, cnt, first, nullptr, perm, undo, sorted, nullptr, 0, n, p.bins_hi, p.hi,
+                      p.lo, st)))
       return e;
   }
   if (runs) {

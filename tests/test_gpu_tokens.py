@@ -65,6 +65,9 @@ EMBED_BWD = [  # rows, vocab, d, dtype, index, skew, holes
     (5000, 1 << 20, 8, BF16, torch.int32, 0.1, 0.1),
     (20000, 300, 264, BF16, torch.int64, 0.9, 0),
     (300, 10, 16384, F32, torch.int64, 0.5, 0),
+    (257, 3, 1032, BF16, torch.int64, 0.9, 0),
+    (65537, 200, 16, BF16, torch.int32, 0.2, 0.1),   # more than the small tiles take
+    (140001, 5000, 8, F32, torch.int64, 0.3, 0.1),   # counts scanned by a kernel of their own
 ]
 
 
@@ -276,6 +279,10 @@ ROUTE = [  # tokens, k, experts, d, dtype, index, dropped
     (3000, 64, 70, 8, BF16, torch.int64, 0.05),
     (2049, 8, 256, 128, F32, torch.int64, 0),
     (5, 3, 2, 16384, BF16, torch.int32, 0.2),
+    (512, 4, 16, 24, BF16, torch.int64, 0.1),         # the most of one tile
+    (683, 3, 9, 24, F32, torch.int64, 0.1),           # one entry more
+    (17001, 8, 300, 8, BF16, torch.int64, 0.1),
+    (70001, 2, 33, 8, F32, torch.int32, 0.1),
 ]
 
 
