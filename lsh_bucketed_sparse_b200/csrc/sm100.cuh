@@ -368,28 +368,11 @@ __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
   return a;
 }
 
+// Arrive on a barrier of another CTA of the cluster.  Orders what tcgen05
+// fences order (tensor memory reads); ordinary writes only within this CTA.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
                : "memory");
-}
-
-// mbar_wait for a barrier that other CTAs of the cluster arrive on.
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity,
-                                                  const volatile int* abort) {
-  const unsigned long long t0 = globaltimer();
-  while (true) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(500000u)
-        : "memory");
-    if (ok) return true;
-    if (*abort) return false;
-    if (globaltimer() - t0 > kWaitLimitNs) return false;
-  }
 }
 
 // A tile to this CTA's shared memory, counted on a barrier of either CTA of

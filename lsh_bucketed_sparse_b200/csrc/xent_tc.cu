@@ -108,6 +108,52 @@ __device__ __forceinline__ uint64_t sdesc_mn(uint32_t saddr) {
          ((uint64_t)(1024 >> 4) << 32) | ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
 }
 
+// Two float32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
+// Largest (or smallest) of 32 values, three operands to an instruction.
+template <bool kMax>
+__device__ __forceinline__ float extreme(const float (&z)[32]) {
+  auto of3 = [](float a, float b, float c) {
+    float r;
+    if (kMax) asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    else asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+  };
+  float a[11];
+#pragma unroll
+  for (int i = 0; i < 10; ++i) a[i] = of3(z[3 * i], z[3 * i + 1], z[3 * i + 2]);
+  a[10] = of3(z[30], z[31], z[31]);
+  const float b0 = of3(a[0], a[1], a[2]), b1 = of3(a[3], a[4], a[5]), b2 = of3(a[6], a[7], a[8]);
+  return of3(of3(b0, b1, b2), a[9], a[10]);
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -177,7 +223,7 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
             const int len = min(it.k1, kc + g.chunk) - kc;
             for (int i = 0; i < len * g.products; ++i, ++n_loads) {
               const int s = n_loads % kStages;
-              if (!mbar_wait_cluster(&empty[s], ((n_loads / kStages) & 1) ^ 1, abort_flag)) {
+              if (!mbar_wait(&empty[s], ((n_loads / kStages) & 1) ^ 1, abort_flag)) {
                 ok = false;
                 break;
               }
@@ -234,14 +280,14 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
             const int blocks = (min(it.k1, kc + g.chunk) - kc) * g.products;
             const int buf = tile & 1;
             const uint32_t d = tmem + buf * kTileN;
-            if (!mbar_wait_cluster(&t_empty[buf], ((tile >> 1) & 1) ^ 1, abort_flag)) {
+            if (!mbar_wait(&t_empty[buf], ((tile >> 1) & 1) ^ 1, abort_flag)) {
               ok = false;
               break;
             }
             tc_fence_after_sync();
             for (int kb = 0; kb < blocks; ++kb, ++n_loads) {
               const int s = n_loads % kStages;
-              if (!mbar_wait_cluster(&full[s], (n_loads / kStages) & 1, abort_flag)) {
+              if (!mbar_wait(&full[s], (n_loads / kStages) & 1, abort_flag)) {
                 ok = false;
                 break;
               }
@@ -341,38 +387,66 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
           }
         }
       }
+      const bool all_there = __all_sync(0xffffffffu, target >= 0);
       // Half h, 32 columns at cc of D, of a 64-column group.
       auto take = [&](float (&z)[32], int h, int cc) {
         if constexpr (kEpi == Epi::kLse) {
           const int there = g.cols - cc;  // columns that exist
           if (there <= 0) return;
-#pragma unroll
-          for (int i = 0; i < 32; ++i) z[i] = i < there ? z[i] * c : -INFINITY;
           if ((unsigned)(target - cc) < 32u) {
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              if (target - cc == i) p.zt[row] = z[i];
+              if (target - cc == i) p.zt[row] = z[i] * c;
           }
-          float top = run_m;
+          if (there >= 32) {
+            const float top = fmaxf(run_m, (c >= 0.f ? extreme<true>(z) : extreme<false>(z)) * c);
+            const float ref = top == -INFINITY ? 0.f : top;
+            const float2 c2 = make_float2(c, c), ref2 = make_float2(-ref, -ref);
+            float2 a[2] = {make_float2(run_s * ex2(run_m - ref), 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-          for (int i = 0; i < 32; ++i) top = fmaxf(top, z[i]);
-          const float ref = top == -INFINITY ? 0.f : top;
-          float a[4] = {run_s * ex2(run_m - ref), 0.f, 0.f, 0.f};
+            for (int i = 0; i < 16; ++i) {
+              const float2 e = fma2(make_float2(z[2 * i], z[2 * i + 1]), c2, ref2);
+              a[i & 1] = add2(a[i & 1], make_float2(ex2(e.x), ex2(e.y)));
+            }
+            run_s = (a[0].x + a[0].y) + (a[1].x + a[1].y);
+            run_m = top;
+          } else {
+            float top = run_m;
 #pragma unroll
-          for (int i = 0; i < 32; ++i) a[i & 3] += ex2(z[i] - ref);
-          run_s = (a[0] + a[1]) + (a[2] + a[3]);
-          run_m = top;
+            for (int i = 0; i < 32; ++i)
+              if (i < there) top = fmaxf(top, z[i] * c);
+            const float ref = top == -INFINITY ? 0.f : top;
+            run_s *= ex2(run_m - ref);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              if (i < there) run_s += ex2(fmaf(z[i], c, -ref));
+            run_m = top;
+          }
         } else if constexpr (kEpi == Epi::kGrad) {
+          const float2 c2 = make_float2(c, c), l2 = make_float2(-lse2, -lse2);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) z[i] = ex2(fmaf(z[i], c, -lse2));
+          for (int i = 0; i < 32; i += 2) {
+            const float2 e = fma2(make_float2(z[i], z[i + 1]), c2, l2);
+            z[i] = ex2(e.x);
+            z[i + 1] = ex2(e.y);
+          }
           const int at = target - p.v0 - cc;
           if ((unsigned)at < 32u) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) z[i] -= at == i ? 1.f : 0.f;
           }
-          // a row without a target takes no part, whatever its logits are
+          const float2 up2 = make_float2(up, up);
 #pragma unroll
-          for (int i = 0; i < 32; ++i) z[i] = target >= 0 ? up * z[i] : 0.f;
+          for (int i = 0; i < 32; i += 2) {
+            const float2 e = mul2(make_float2(z[i], z[i + 1]), up2);
+            z[i] = e.x;
+            z[i + 1] = e.y;
+          }
+          // a row without a target takes no part, whatever its logits are
+          if (!all_there && target < 0) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) z[i] = 0.f;
+          }
           if constexpr (kPlanes) {
 #pragma unroll
             for (int pl = 0; pl < 3; ++pl) {
@@ -404,46 +478,67 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
       for (int n = it.n0; ok && n < it.n1; ++n) {
         const int nw = n == g.n_tiles - 1 ? g.last_width : g.width;
         const int groups = (nw + 63) / 64, col0 = n * g.width;
-        // One accumulator, or with planes the chunks' accumulators added up
-        // in registers (round to nearest, where the tensor core truncates).
-        float sum[2][2][32];
-        for (int kc = it.k0; ok && kc < it.k1; kc += g.chunk, ++tile) {
+        // this warp's 32-column chunks: halves of the groups half, half + 2
+        const int chunks = groups > half + 2 ? 4 : groups > half ? 2 : 0;
+        auto chunk_col = [&](int i) { return (half + (i & 2)) * 64 + (i & 1) * 32; };
+        if constexpr (!kPlanes) {
           const int buf = tile & 1;
-          if (!mbar_wait_cluster(&t_full[buf], (tile >> 1) & 1, abort_flag)) { ok = false; break; }
+          if (!mbar_wait(&t_full[buf], (tile >> 1) & 1, abort_flag)) { ok = false; break; }
           __syncwarp();
           tc_fence_after_sync();
-#pragma unroll kPlanes ? 2 : 1
-          for (int gi = 0; gi < 2; ++gi) {
-            const int q = half + 2 * gi;
-            if (q >= groups) continue;
+          const uint32_t from = lane_addr + (uint32_t)(buf * kTileN);
+          uint32_t u[2][32];
+          if (chunks) {
+            tmem_ld_32x32b_x32(from + (uint32_t)chunk_col(0), u[0]);
+            tmem_ld_wait(u[0]);
+          }
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              uint32_t u[32];
-              const int col = q * 64 + h * 32;
-              tmem_ld_32x32b_x32(lane_addr + (uint32_t)(buf * kTileN + col), u);
-              tmem_ld_wait(u);
-              if constexpr (kPlanes) {
+          for (int i = 0; i < 4; ++i) {
+            if (i >= chunks) break;
+            // the next chunk comes while this one is taken
+            if (i + 1 < chunks) {
+              __syncwarp();
+              tmem_ld_32x32b_x32(from + (uint32_t)chunk_col(i + 1), u[(i + 1) & 1]);
+            }
+            float z[32];
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  sum[gi][h][i] = __uint_as_float(u[i]) + (kc == it.k0 ? 0.f : sum[gi][h][i]);
-              } else {
-                float z[32];
-#pragma unroll
-                for (int i = 0; i < 32; ++i) z[i] = __uint_as_float(u[i]);
-                take(z, h, col0 + col);
-              }
+            for (int j = 0; j < 32; ++j) z[j] = __uint_as_float(u[i & 1][j]);
+            take(z, i & 1, col0 + chunk_col(i));
+            if (i + 1 < chunks) {
+              __syncwarp();
+              tmem_ld_wait(u[(i + 1) & 1]);
+              // (the last one is here: the accumulator is free)
+              if (i + 2 == chunks) release(buf);
             }
           }
-          release(buf);
-        }
-        if constexpr (kPlanes) {
+          if (chunks == 0) release(buf);
+          ++tile;
+        } else {
+          // the accumulators of the chunks of K are added up in registers (round
+          // to nearest, where the tensor core truncates)
+          float sum[4][32];
+          for (int kc = it.k0; ok && kc < it.k1; kc += g.chunk, ++tile) {
+            const int buf = tile & 1;
+            if (!mbar_wait(&t_full[buf], (tile >> 1) & 1, abort_flag)) { ok = false; break; }
+            __syncwarp();
+            tc_fence_after_sync();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if (i >= chunks) break;
+              uint32_t u[32];
+              tmem_ld_32x32b_x32(lane_addr + (uint32_t)(buf * kTileN + chunk_col(i)), u);
+              tmem_ld_wait(u);
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                sum[i][j] = __uint_as_float(u[j]) + (kc == it.k0 ? 0.f : sum[i][j]);
+            }
+            release(buf);
+          }
           if (!ok) break;
 #pragma unroll
-          for (int gi = 0; gi < 2; ++gi) {
-            if (half + 2 * gi >= groups) continue;
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-              take(sum[gi][h], h, col0 + (half + 2 * gi) * 64 + h * 32);
+          for (int i = 0; i < 4; ++i) {
+            if (i >= chunks) break;
+            take(sum[i], i & 1, col0 + chunk_col(i));
           }
         }
       }
