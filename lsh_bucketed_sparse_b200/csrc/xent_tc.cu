@@ -611,17 +611,11 @@ size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 int pairs_of_device() { return std::max(1, sm_count() / 2); }
 
-// Columns of D cut into tiles of `width`, a multiple of 64: the fewest that
-// 256 allows, or more of them while pairs would stand idle.
-void set_columns(Gemm* g, int cols) {
-  g->cols = cols;
-  const int fewest = ceil_div(cols, kTileN);
-  const int idle = ceil_div(pairs_of_device(), g->m_tiles);
-  const int n = std::max(fewest, std::min(ceil_div(cols, 64), idle));
-  g->width = ceil_div(ceil_div(cols, n), 64) * 64;
-  g->n_tiles = ceil_div(cols, g->width);
-  g->last_width = ceil_div(cols - (g->n_tiles - 1) * g->width, 32) * 32;  // N of a pair's MMA
-}
+// Clock cycles per K block of a tile of `width` columns: the pair's tensor
+// cores take 2 per column, but what a CTA has to fetch for it (16 KB of A, half
+// the columns of B) comes at some 48 bytes a cycle.
+double block_cycles(int width) { return std::max(2.0 * width, 341 + 1.33 * width); }
+constexpr double kTileCycles = 3000;  // to fill and empty the pipeline
 
 // K blocks per accumulator.  The tensor core truncates when it adds to one, an
 // error that grows with the number of additions (1.1e-5 of dx after 500 of
@@ -633,22 +627,50 @@ void set_chunk(Gemm* g) {
   if (g->products > 1) g->chunk = ceil_div(g->kb_split, ceil_div(g->kb_split, kPlaneChunk));
 }
 
-Gemm make_gemm(long long rows, int cols, int k, bool f32, bool a_mn, bool b_mn) {
+// Cuts D's columns into tiles (of a multiple of 64) and K into parts (with
+// may_split) so that the estimated time is least: fewer columns or a part of K
+// per tile where whole tiles would leave pairs idle.  A part of K costs
+// another plane of partial sums, written and read back at HBM's rate (some
+// 4000 bytes per cycle).
+void set_tiles(Gemm* g, bool may_split) {
+  const int pairs = pairs_of_device();
+  double best = -1;
+  for (int width = kTileN; width >= 64; width -= 64) {
+    const int n = ceil_div(g->cols, width), last = g->cols - (n - 1) * width;
+    const int last_width = ceil_div(last, 32) * 32;  // N of a pair's MMA
+    const double block = (block_cycles(width) * (n - 1) + block_cycles(last_width)) / n;
+    for (int s = 1; s <= (may_split ? 8 : 1) && s <= g->kb; ++s) {
+      const int kb = ceil_div(g->kb, s);
+      if (ceil_div(g->kb, kb) != s) continue;
+      const double waves = ceil_div((long long)g->m_tiles * n * s, pairs);
+      const double cost = waves * (kb * g->products * block + kTileCycles) +
+                          (s > 1 ? 2.0 * s * g->rows * g->cols * 4 / 4000 : 0.0);
+      if (best >= 0 && cost >= best) continue;
+      best = cost;
+      g->width = width;
+      g->n_tiles = n;
+      g->last_width = last_width;
+      g->splits = s;
+      g->kb_split = kb;
+    }
+  }
+  g->run = 1;
+  g->slices = g->n_tiles;
+  g->items = g->m_tiles * g->n_tiles * g->splits;
+  set_chunk(g);
+}
+
+Gemm make_gemm(long long rows, int cols, int k, bool f32, bool a_mn, bool b_mn, bool may_split) {
   Gemm g = {};
   g.rows = (int)rows;
+  g.cols = cols;
   g.m_tiles = ceil_div(rows, kTileM);
-  set_columns(&g, cols);
-  g.run = 1;
-  g.slices = g.n_tiles;
   g.kb = ceil_div(k, kBlockK);
-  g.splits = 1;
-  g.kb_split = g.kb;
   g.products = f32 ? 6 : 1;
-  set_chunk(&g);
   g.group = 16;
-  g.items = g.m_tiles * g.slices;
   g.a_mn = a_mn;
   g.b_mn = b_mn;
+  set_tiles(&g, may_split);
   return g;
 }
 
@@ -656,7 +678,7 @@ Gemm make_gemm(long long rows, int cols, int k, bool f32, bool a_mn, bool b_mn) 
 // partial results per row.  The longest run that costs at most 2% more time
 // than the best one.
 Gemm logits_gemm(const TableProblem& p) {
-  Gemm g = make_gemm(p.rows, p.vocab, p.d, !p.bf16, false, false);
+  Gemm g = make_gemm(p.rows, p.vocab, p.d, !p.bf16, false, false, false);
   const int pairs = pairs_of_device();
   auto span = [&](int run) {
     return (long long)ceil_div((long long)g.m_tiles * ceil_div(g.n_tiles, run), pairs) * run;
@@ -672,52 +694,17 @@ Gemm logits_gemm(const TableProblem& p) {
   return g;
 }
 
-// Cut K where whole tiles would leave pairs idle: cost in blocks of K, with
-// kTileCost blocks to fill and empty the pipeline per tile and the time of the
-// partial sums' traffic (a block takes about 0.35 us, HBM moves about 2 MB in that).
-void set_splits(Gemm* g) {
-  constexpr int kTileCost = 6;
-  const int pairs = pairs_of_device(), tiles = g->m_tiles * g->n_tiles;
-  const double plane = (double)g->rows * g->cols * 4 / 2e6;
-  double best = 0;
-  for (int s = 1; s <= 8 && s <= g->kb; ++s) {
-    const int kb = ceil_div(g->kb, s);
-    if (ceil_div(g->kb, kb) != s) continue;
-    const double cost = (double)ceil_div((long long)tiles * s, pairs) * (kb * g->products + kTileCost) +
-                        (s > 1 ? 2 * s * plane : 0.0);
-    if (s == 1 || cost < best) {
-      best = cost;
-      g->splits = s;
-      g->kb_split = kb;
-    }
-  }
-  g->items = g->m_tiles * g->n_tiles * g->splits;
-  set_chunk(g);
-}
-
 // The backward's pieces: g of `words` columns (a multiple of 256) within
 // kGradBytes.  Among those, the count whose pieces take the fewest waves of
 // dW tiles, then the largest.
-constexpr size_t kGradBytes = 512u << 20;
+constexpr size_t kGradBytes = 640u << 20;
 struct Backward {
   int words, pieces;
   size_t ld;             // columns of g
   bool sum_dx, sum_dw;   // float32 sums outside the results
-  int dx_splits, dw_splits;
+  Gemm dx, dw;           // of a whole piece
   size_t clean, w_planes, g, dx_sums, dw_sums, total;
 };
-
-Gemm dx_gemm(const TableProblem& p, int words) {
-  Gemm g = make_gemm(p.rows, p.d, words, !p.bf16, false, true);
-  set_splits(&g);
-  return g;
-}
-
-Gemm dw_gemm(const TableProblem& p, int words) {
-  Gemm g = make_gemm(words, p.d, (int)p.rows, !p.bf16, true, true);
-  set_splits(&g);
-  return g;
-}
 
 Backward plan_backward(const TableProblem& p) {
   Backward b;
@@ -738,19 +725,19 @@ Backward plan_backward(const TableProblem& p) {
   b.words = tiles * kTileM;
   b.pieces = ceil_div(all, tiles);
   b.ld = (size_t)b.words;
-  // splits are fixed by the full pieces; the last one, if shorter, keeps them
-  b.dx_splits = dx_gemm(p, b.pieces == 1 ? p.vocab : b.words).splits;
-  b.dw_splits = dw_gemm(p, b.pieces == 1 ? p.vocab : b.words).splits;
+  const int words = std::min(b.words, p.vocab);
+  b.dx = make_gemm(p.rows, p.d, words, !p.bf16, false, true, true);
+  b.dw = make_gemm(words, p.d, (int)p.rows, !p.bf16, true, true, true);
   // with float32 results and no split K the result itself is the sum
-  b.sum_dx = b.dx_splits > 1 || (b.pieces > 1 && p.bf16);
-  b.sum_dw = b.dw_splits > 1;
+  b.sum_dx = b.dx.splits > 1 || (b.pieces > 1 && p.bf16);
+  b.sum_dw = b.dw.splits > 1;
   const size_t nd = (size_t)p.rows * p.d, vd = (size_t)b.words * p.d;
   size_t off = 0;
   b.clean = off;    off += align256(nd * 2 * planes);
   b.w_planes = off; off += p.bf16 ? 0 : align256((size_t)p.vocab * p.d * 6);
   b.g = off;        off += align256((size_t)planes * p.rows * b.ld * 2);
-  b.dx_sums = off;  off += b.sum_dx ? align256(nd * 4 * b.dx_splits) : 0;
-  b.dw_sums = off;  off += b.sum_dw ? align256(vd * 4 * b.dw_splits) : 0;
+  b.dx_sums = off;  off += b.sum_dx ? align256(nd * 4 * b.dx.splits) : 0;
+  b.dw_sums = off;  off += b.sum_dw ? align256(vd * 4 * b.dw.splits) : 0;
   b.total = off;
   return b;
 }
@@ -916,7 +903,7 @@ cudaError_t launch_xent_tc_backward(const TableProblem& p, const void* x, const 
     const char* wv = static_cast<const char*>(w) + (size_t)v0 * p.d * 2;
     // g of the piece
     Params k = {};
-    k.g = make_gemm(p.rows, nv, p.d, f32, false, false);
+    k.g = make_gemm(p.rows, nv, p.d, f32, false, false, false);
     k.err = err;
     k.targets = targets;
     k.scale = p.scale;
@@ -934,20 +921,20 @@ cudaError_t launch_xent_tc_backward(const TableProblem& p, const void* x, const 
       return cudaErrorInvalidValue;
     if ((e = launch_logits<Epi::kGrad>(p.idx64, x_k, w_k, g_out, k, st))) return e;
     // dx += g W
-    Gemm gx = make_gemm(p.rows, p.d, nv, f32, false, true);
-    // (a last, shorter piece may have blocks for fewer parts only)
-    gx.kb_split = ceil_div(gx.kb, plan.dx_splits);
+    // (the first piece's cut; a last, shorter one may have blocks for fewer parts)
+    Gemm gx = plan.dx;
+    gx.kb = ceil_div(nv, kBlockK);
+    gx.kb_split = ceil_div(gx.kb, plan.dx.splits);
     gx.splits = ceil_div(gx.kb, gx.kb_split);
-    set_chunk(&gx);
     gx.items = gx.m_tiles * gx.n_tiles * gx.splits;
+    set_chunk(&gx);
     void* dx_to = plan.sum_dx ? static_cast<void*>(dx_sums) : dx;
     if ((e = launch_product(gx, g_k, w_mn, dx_to, f32 || plan.sum_dx, p.d, p.rows, v0 > 0, err, st)))
       return e;
     // dW = g^T x
-    Gemm gw = make_gemm(nv, p.d, (int)p.rows, f32, true, true);
-    gw.splits = plan.dw_splits;
-    gw.kb_split = ceil_div(gw.kb, gw.splits);
-    set_chunk(&gw);
+    Gemm gw = plan.dw;
+    gw.rows = nv;
+    gw.m_tiles = ceil_div(nv, kTileM);
     gw.items = gw.m_tiles * gw.n_tiles * gw.splits;
     char* dw_at = static_cast<char*>(dtable) + (size_t)v0 * p.d * p.elem();
     void* dw_to = plan.sum_dw ? static_cast<void*>(dw_sums) : dw_at;
@@ -958,7 +945,7 @@ cudaError_t launch_xent_tc_backward(const TableProblem& p, const void* x, const 
       return e;
   }
   if (plan.sum_dx)
-    return launch_sum(p.bf16, dx_sums, dx, p.rows * p.d, plan.dx_splits, st);
+    return launch_sum(p.bf16, dx_sums, dx, p.rows * p.d, plan.dx.splits, st);
   return cudaSuccess;
 }
 
