@@ -35,13 +35,19 @@ using namespace sm100;
 constexpr int kTileM = 256;   // rows of a pair's tile, 128 per CTA
 constexpr int kTileN = 256;   // most columns of a tile
 constexpr int kBlockK = 64;   // one 128-byte swizzled row of bf16
-constexpr int kStages = 6;
-constexpr int kOperand = 128 * kBlockK * 2;  // bytes of one CTA's A or B in a stage
+constexpr int kOperand = 128 * kBlockK * 2;  // bytes of one CTA's A or B of a K block
+// A stage holds a K block of A and B, of all three planes of float32 operands
+// (each is used by two or three of the six products).
+constexpr int kRing = 12;  // operands in the ring of stages
+__host__ __device__ constexpr int stage_operands(bool planes) { return planes ? 6 : 2; }
+__host__ __device__ constexpr int stage_count(bool planes) {
+  return kRing / stage_operands(planes);
+}
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = (2 + kEpiWarps) * 32;
 constexpr int kStaging = 32 * 128;  // bytes per epilogue warp: 32 rows of 128 bytes
-constexpr int kBars = 2 * kStages + 5;
-constexpr int kSmem = 1024 + kStages * 2 * kOperand + kEpiWarps * kStaging + kBars * 8 + 16;
+constexpr int kBars = 2 * stage_count(false) + 5;
+constexpr int kSmem = 1024 + kRing * kOperand + kEpiWarps * kStaging + kBars * 8 + 16;
 static_assert(kSmem <= 227 * 1024, "shared memory");
 
 enum class Epi { kLse, kGrad, kStore, kAdd };
@@ -52,7 +58,7 @@ struct Gemm {
   int run, slices;        // n tiles of one work item, items per m tile
   int splits, kb_split;   // K in `splits` parts of kb_split blocks
   int kb;                 // K blocks of 64
-  int products;           // 1, or the 6 of three planes each
+  bool planes;            // float32 operands
   int chunk;              // K blocks summed in one accumulator
   int group;              // m tiles that are walked together
   int items;
@@ -94,12 +100,9 @@ __device__ __forceinline__ Item decode(const Gemm& g, int item) {
 
 // Planes of A and B in product i of a float32 product, two bits each, smallest
 // products first: (0,2) (2,0) (1,1) (0,1) (1,0) (0,0).
-__device__ __forceinline__ int plane_a(int products, int i) {
-  return products == 1 ? 0 : (0x0118 >> (2 * i)) & 3;
-}
-__device__ __forceinline__ int plane_b(int products, int i) {
-  return products == 1 ? 0 : (0x0052 >> (2 * i)) & 3;
-}
+constexpr int kProducts = 6;
+__device__ __forceinline__ int plane_a(int i) { return (0x0118 >> (2 * i)) & 3; }
+__device__ __forceinline__ int plane_b(int i) { return (0x0052 >> (2 * i)) & 3; }
 
 // MN-major operand, 128-byte swizzle: rows of 64 elements of M or N (one row
 // per k), groups of 8 k 1024 bytes apart, the next 64 elements 8192 bytes on.
@@ -168,9 +171,9 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  uint8_t* a_smem = smem;
-  uint8_t* b_smem = smem + kStages * kOperand;
-  uint8_t* staging = smem + 2 * kStages * kOperand;
+  constexpr int kStages = stage_count(kPlanes), kOps = kPlanes ? 3 : 1;
+  constexpr int kStageBytes = stage_operands(kPlanes) * kOperand;  // A's planes, then B's
+  uint8_t* staging = smem + kRing * kOperand;
   uint64_t* full = reinterpret_cast<uint64_t*>(staging + kEpiWarps * kStaging);  // CTA 0's
   uint64_t* empty = full + kStages;
   uint64_t* t_full = empty + kStages;   // [2]
@@ -210,7 +213,7 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
       tma_prefetch_desc(&bmap);
       const int b_boxes = g.b_mn ? (g.width / 2 + 63) / 64 : 1;
       const uint32_t b_bytes = g.b_mn ? b_boxes * 8192 : g.width / 2 * 128;
-      const uint32_t bytes = 2 * (kOperand + b_bytes);  // of both CTAs
+      const uint32_t bytes = 2 * kOps * (kOperand + b_bytes);  // of both CTAs
       int n_loads = 0;
       bool ok = true;
       for (int item = pair; ok && item < g.items; item += pairs) {
@@ -219,32 +222,30 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
         for (int n = it.n0; ok && n < it.n1; ++n) {
           const int nw = n == g.n_tiles - 1 ? g.last_width : g.width;
           const int c0 = n * g.width + rank * (nw / 2);
-          for (int kc = it.k0; ok && kc < it.k1; kc += g.chunk) {
-            const int len = min(it.k1, kc + g.chunk) - kc;
-            for (int i = 0; i < len * g.products; ++i, ++n_loads) {
-              const int s = n_loads % kStages;
-              if (!mbar_wait(&empty[s], ((n_loads / kStages) & 1) ^ 1, abort_flag)) {
-                ok = false;
-                break;
-              }
-              if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
-              const uint32_t bar = cluster_addr(&full[s], 0);
-              uint8_t* a = a_smem + s * kOperand;
-              uint8_t* b = b_smem + s * kOperand;
-              const int pr = g.products > 1 ? i / len : 0;
-              const int k = (kc + i - pr * len) * kBlockK;
-              const int za = plane_a(g.products, pr), zb = plane_b(g.products, pr);
+          for (int kb = it.k0; kb < it.k1; ++kb, ++n_loads) {
+            const int s = n_loads % kStages;
+            if (!mbar_wait(&empty[s], ((n_loads / kStages) & 1) ^ 1, abort_flag)) {
+              ok = false;
+              break;
+            }
+            if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
+            const uint32_t bar = cluster_addr(&full[s], 0);
+            const int k = kb * kBlockK;
+#pragma unroll
+            for (int z = 0; z < kOps; ++z) {
+              uint8_t* a = smem + s * kStageBytes + z * kOperand;
+              uint8_t* b = a + kOps * kOperand;
               if (g.a_mn) {
-                tma_load_3d_pair(a, &amap, bar, m0, k, za);
-                tma_load_3d_pair(a + 8192, &amap, bar, m0 + 64, k, za);
+                tma_load_3d_pair(a, &amap, bar, m0, k, z);
+                tma_load_3d_pair(a + 8192, &amap, bar, m0 + 64, k, z);
               } else {
-                tma_load_3d_pair(a, &amap, bar, k, m0, za);
+                tma_load_3d_pair(a, &amap, bar, k, m0, z);
               }
               if (g.b_mn) {
                 for (int j = 0; j < b_boxes; ++j)
-                  tma_load_3d_pair(b + j * 8192, &bmap, bar, c0 + 64 * j, k, zb);
+                  tma_load_3d_pair(b + j * 8192, &bmap, bar, c0 + 64 * j, k, z);
               } else {
-                tma_load_3d_pair(b, &bmap, bar, k, c0, zb);
+                tma_load_3d_pair(b, &bmap, bar, k, c0, z);
               }
             }
           }
@@ -277,7 +278,7 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
           const int nw = n == g.n_tiles - 1 ? g.last_width : g.width;
           const uint32_t idesc = idesc_bf16_f32(kTileM, nw) | major;
           for (int kc = it.k0; ok && kc < it.k1; kc += g.chunk, ++tile) {
-            const int blocks = (min(it.k1, kc + g.chunk) - kc) * g.products;
+            const int blocks = min(it.k1, kc + g.chunk) - kc;
             const int buf = tile & 1;
             const uint32_t d = tmem + buf * kTileN;
             if (!mbar_wait(&t_empty[buf], ((tile >> 1) & 1) ^ 1, abort_flag)) {
@@ -292,14 +293,17 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
                 break;
               }
               tc_fence_after_sync();
-              const uint32_t a = smem_u32(a_smem + s * kOperand);
-              const uint32_t b = smem_u32(b_smem + s * kOperand);
+              const uint32_t a0 = smem_u32(smem + s * kStageBytes), b0 = a0 + kOps * kOperand;
+              for (int i = 0; i < (kPlanes ? kProducts : 1); ++i) {
+                const uint32_t a = kPlanes ? a0 + plane_a(i) * kOperand : a0;
+                const uint32_t b = kPlanes ? b0 + plane_b(i) * kOperand : b0;
 #pragma unroll
-              for (int k = 0; k < kBlockK / 16; ++k) {
-                const uint32_t ak = a + k * a_step, bk = b + k * b_step;
-                mma_bf16_ss_pair(d, g.a_mn ? sdesc_mn(ak) : sdesc_kmajor_sw128(ak),
-                                 g.b_mn ? sdesc_mn(bk) : sdesc_kmajor_sw128(bk), idesc,
-                                 kb > 0 || k > 0);
+                for (int k = 0; k < kBlockK / 16; ++k) {
+                  const uint32_t ak = a + k * a_step, bk = b + k * b_step;
+                  mma_bf16_ss_pair(d, g.a_mn ? sdesc_mn(ak) : sdesc_kmajor_sw128(ak),
+                                   g.b_mn ? sdesc_mn(bk) : sdesc_kmajor_sw128(bk), idesc,
+                                   kb > 0 || i > 0 || k > 0);
+                }
               }
               issued = true;
               mma_commit_pair(&empty[s]);
@@ -612,20 +616,21 @@ int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 int pairs_of_device() { return std::max(1, sm_count() / 2); }
 
 // Clock cycles per K block of a tile of `width` columns: the pair's tensor
-// cores take 2 per column, but what a CTA has to fetch for it (16 KB of A, half
-// the columns of B) comes at some 48 bytes a cycle.
-double block_cycles(int width) { return std::max(2.0 * width, 341 + 1.33 * width); }
+// cores take 2 per column and product, but what a CTA has to fetch for it
+// (16 KB of A, half the columns of B, of each plane) comes at some 48 bytes a
+// cycle.
+double block_cycles(int width, bool planes) {
+  return planes ? std::max(2.0 * kProducts * width, 3 * (341 + 1.33 * width))
+                : std::max(2.0 * width, 341 + 1.33 * width);
+}
 constexpr double kTileCycles = 3000;  // to fill and empty the pipeline
 
 // K blocks per accumulator.  The tensor core truncates when it adds to one, an
-// error that grows with the number of additions (1.1e-5 of dx after 500 of
-// them): float32 operands get a new accumulator after kPlaneChunk blocks, 32
-// additions of the largest products.
-constexpr int kPlaneChunk = 8;
-void set_chunk(Gemm* g) {
-  g->chunk = g->kb_split;
-  if (g->products > 1) g->chunk = ceil_div(g->kb_split, ceil_div(g->kb_split, kPlaneChunk));
-}
+// error that grows with the number of additions to a sum of full size (1.1e-5
+// of dx after 500 of them): float32 operands get a new accumulator after
+// kPlaneChunk blocks, 28 such additions.
+constexpr int kPlaneChunk = 2;
+void set_chunk(Gemm* g) { g->chunk = g->planes ? kPlaneChunk : g->kb_split; }
 
 // Cuts D's columns into tiles (of a multiple of 64) and K into parts (with
 // may_split) so that the estimated time is least: fewer columns or a part of K
@@ -638,12 +643,13 @@ void set_tiles(Gemm* g, bool may_split) {
   for (int width = kTileN; width >= 64; width -= 64) {
     const int n = ceil_div(g->cols, width), last = g->cols - (n - 1) * width;
     const int last_width = ceil_div(last, 32) * 32;  // N of a pair's MMA
-    const double block = (block_cycles(width) * (n - 1) + block_cycles(last_width)) / n;
+    const double block = (block_cycles(width, g->planes) * (n - 1) +
+                          block_cycles(last_width, g->planes)) / n;
     for (int s = 1; s <= (may_split ? 8 : 1) && s <= g->kb; ++s) {
       const int kb = ceil_div(g->kb, s);
       if (ceil_div(g->kb, kb) != s) continue;
       const double waves = ceil_div((long long)g->m_tiles * n * s, pairs);
-      const double cost = waves * (kb * g->products * block + kTileCycles) +
+      const double cost = waves * (kb * block + kTileCycles) +
                           (s > 1 ? 2.0 * s * g->rows * g->cols * 4 / 4000 : 0.0);
       if (best >= 0 && cost >= best) continue;
       best = cost;
@@ -666,7 +672,7 @@ Gemm make_gemm(long long rows, int cols, int k, bool f32, bool a_mn, bool b_mn, 
   g.cols = cols;
   g.m_tiles = ceil_div(rows, kTileM);
   g.kb = ceil_div(k, kBlockK);
-  g.products = f32 ? 6 : 1;
+  g.planes = f32;
   g.group = 16;
   g.a_mn = a_mn;
   g.b_mn = b_mn;
@@ -775,7 +781,7 @@ cudaError_t launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap
 template <Epi kEpi>
 cudaError_t launch_logits(bool idx64, const CUtensorMap& a, const CUtensorMap& b,
                           const CUtensorMap& o, const Params& p, cudaStream_t st) {
-  if (p.g.products == 1)
+  if (!p.g.planes)
     return idx64 ? launch<kEpi, __nv_bfloat16, int64_t, false>(a, b, o, p, st)
                  : launch<kEpi, __nv_bfloat16, int32_t, false>(a, b, o, p, st);
   return idx64 ? launch<kEpi, float, int64_t, true>(a, b, o, p, st)
@@ -821,7 +827,7 @@ cudaError_t launch_product(const Gemm& g, const CUtensorMap& a, const CUtensorMa
   p.g = g;
   p.err = err;
   if (!f32) return launch<Epi::kStore, __nv_bfloat16, int32_t, false>(a, b, o, p, st);
-  if (g.products == 1)
+  if (!g.planes)
     return add ? launch<Epi::kAdd, float, int32_t, false>(a, b, o, p, st)
                : launch<Epi::kStore, float, int32_t, false>(a, b, o, p, st);
   return add ? launch<Epi::kAdd, float, int32_t, true>(a, b, o, p, st)
