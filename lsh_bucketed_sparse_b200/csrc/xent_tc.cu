@@ -8,7 +8,7 @@
 // its 128 rows of A and its half of B's columns, 64 of K at a time, and holds
 // its 128 rows of D in tensor memory, twice, so that the next tile's products
 // run while the epilogue reads the last one.  Per CTA:
-//   warp 0      TMA loads into a ring of kStages stages;
+//   warp 0      TMA loads into a ring of kSlots slots;
 //   warp 1      allocates tensor memory; in CTA 0 one thread issues the MMAs;
 //   warps 2..9  epilogue, two warps per quadrant of TMEM lanes, which share a
 //               tile's 64-column groups between them.
@@ -36,18 +36,15 @@ constexpr int kTileM = 256;   // rows of a pair's tile, 128 per CTA
 constexpr int kTileN = 256;   // most columns of a tile
 constexpr int kBlockK = 64;   // one 128-byte swizzled row of bf16
 constexpr int kOperand = 128 * kBlockK * 2;  // bytes of one CTA's A or B of a K block
-// A stage holds a K block of A and B, of all three planes of float32 operands
-// (each is used by two or three of the six products).
-constexpr int kRing = 12;  // operands in the ring of stages
-__host__ __device__ constexpr int stage_operands(bool planes) { return planes ? 6 : 2; }
-__host__ __device__ constexpr int stage_count(bool planes) {
-  return kRing / stage_operands(planes);
-}
+// The ring's slots hold A and B of a K block, with float32 operands one plane
+// of them (each is used by two or three of the six products): 6 or 2 K blocks.
+constexpr int kSlots = 6;
+constexpr int kSlotBytes = 2 * kOperand;
 constexpr int kEpiWarps = 8;
 constexpr int kThreads = (2 + kEpiWarps) * 32;
 constexpr int kStaging = 32 * 128;  // bytes per epilogue warp: 32 rows of 128 bytes
-constexpr int kBars = 2 * stage_count(false) + 5;
-constexpr int kSmem = 1024 + kRing * kOperand + kEpiWarps * kStaging + kBars * 8 + 16;
+constexpr int kBars = 2 * kSlots + 5;
+constexpr int kSmem = 1024 + kSlots * kSlotBytes + kEpiWarps * kStaging + kBars * 8 + 16;
 static_assert(kSmem <= 227 * 1024, "shared memory");
 
 enum class Epi { kLse, kGrad, kStore, kAdd };
@@ -97,12 +94,6 @@ __device__ __forceinline__ Item decode(const Gemm& g, int item) {
   it.k1 = min(g.kb, it.k0 + g.kb_split);
   return it;
 }
-
-// Planes of A and B in product i of a float32 product, two bits each, smallest
-// products first: (0,2) (2,0) (1,1) (0,1) (1,0) (0,0).
-constexpr int kProducts = 6;
-__device__ __forceinline__ int plane_a(int i) { return (0x0118 >> (2 * i)) & 3; }
-__device__ __forceinline__ int plane_b(int i) { return (0x0052 >> (2 * i)) & 3; }
 
 // MN-major operand, 128-byte swizzle: rows of 64 elements of M or N (one row
 // per k), groups of 8 k 1024 bytes apart, the next 64 elements 8192 bytes on.
@@ -171,12 +162,11 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  constexpr int kStages = stage_count(kPlanes), kOps = kPlanes ? 3 : 1;
-  constexpr int kStageBytes = stage_operands(kPlanes) * kOperand;  // A's planes, then B's
-  uint8_t* staging = smem + kRing * kOperand;
+  constexpr int kOps = kPlanes ? 3 : 1, kDepth = kSlots / kOps;  // slots per K block, K blocks
+  uint8_t* staging = smem + kSlots * kSlotBytes;
   uint64_t* full = reinterpret_cast<uint64_t*>(staging + kEpiWarps * kStaging);  // CTA 0's
-  uint64_t* empty = full + kStages;
-  uint64_t* t_full = empty + kStages;   // [2]
+  uint64_t* empty = full + kSlots;
+  uint64_t* t_full = empty + kSlots;   // [2]
   uint64_t* t_empty = t_full + 2;       // [2], CTA 0's
   uint64_t* done = t_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
@@ -187,7 +177,7 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < kSlots; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
@@ -213,7 +203,7 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
       tma_prefetch_desc(&bmap);
       const int b_boxes = g.b_mn ? (g.width / 2 + 63) / 64 : 1;
       const uint32_t b_bytes = g.b_mn ? b_boxes * 8192 : g.width / 2 * 128;
-      const uint32_t bytes = 2 * kOps * (kOperand + b_bytes);  // of both CTAs
+      const uint32_t bytes = 2 * (kOperand + b_bytes);  // of both CTAs
       int n_loads = 0;
       bool ok = true;
       for (int item = pair; ok && item < g.items; item += pairs) {
@@ -222,19 +212,20 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
         for (int n = it.n0; ok && n < it.n1; ++n) {
           const int nw = n == g.n_tiles - 1 ? g.last_width : g.width;
           const int c0 = n * g.width + rank * (nw / 2);
-          for (int kb = it.k0; kb < it.k1; ++kb, ++n_loads) {
-            const int s = n_loads % kStages;
-            if (!mbar_wait(&empty[s], ((n_loads / kStages) & 1) ^ 1, abort_flag)) {
-              ok = false;
-              break;
-            }
-            if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
-            const uint32_t bar = cluster_addr(&full[s], 0);
+          for (int kb = it.k0; ok && kb < it.k1; ++kb, ++n_loads) {
             const int k = kb * kBlockK;
+            // planes in the order in which their slots become free
 #pragma unroll
-            for (int z = 0; z < kOps; ++z) {
-              uint8_t* a = smem + s * kStageBytes + z * kOperand;
-              uint8_t* b = a + kOps * kOperand;
+            for (int z = kOps - 1; z >= 0; --z) {
+              const int s = n_loads % kDepth * kOps + z;
+              if (!mbar_wait(&empty[s], ((n_loads / kDepth) & 1) ^ 1, abort_flag)) {
+                ok = false;
+                break;
+              }
+              if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
+              const uint32_t bar = cluster_addr(&full[s], 0);
+              uint8_t* a = smem + s * kSlotBytes;
+              uint8_t* b = a + kOperand;
               if (g.a_mn) {
                 tma_load_3d_pair(a, &amap, bar, m0, k, z);
                 tma_load_3d_pair(a + 8192, &amap, bar, m0 + 64, k, z);
@@ -258,12 +249,13 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
       // The last loads must land before either CTA may exit (CTA 1 waits for
       // CTA 0 at the end).
       if (rank == 0)
-        for (int l = n_loads > kStages ? n_loads - kStages : 0; l < n_loads; ++l) {
-          const unsigned long long t0 = globaltimer();
-          while (!mbar_try_wait(&full[l % kStages], (l / kStages) & 1)) {
-            if (globaltimer() - t0 > kWaitLimitNs) { atomicOr(p.err, kErrWaitDrain); break; }
+        for (int l = n_loads > kDepth ? n_loads - kDepth : 0; l < n_loads; ++l)
+          for (int z = 0; z < kOps; ++z) {
+            const unsigned long long t0 = globaltimer();
+            while (!mbar_try_wait(&full[l % kDepth * kOps + z], (l / kDepth) & 1)) {
+              if (globaltimer() - t0 > kWaitLimitNs) { atomicOr(p.err, kErrWaitDrain); break; }
+            }
           }
-        }
     }
   } else if (warp == 1) {
     // -------------------------------------------------------------- MMAs
@@ -286,27 +278,44 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
               break;
             }
             tc_fence_after_sync();
-            for (int kb = 0; kb < blocks; ++kb, ++n_loads) {
-              const int s = n_loads % kStages;
-              if (!mbar_wait(&full[s], (n_loads / kStages) & 1, abort_flag)) {
-                ok = false;
-                break;
-              }
-              tc_fence_after_sync();
-              const uint32_t a0 = smem_u32(smem + s * kStageBytes), b0 = a0 + kOps * kOperand;
-              for (int i = 0; i < (kPlanes ? kProducts : 1); ++i) {
-                const uint32_t a = kPlanes ? a0 + plane_a(i) * kOperand : a0;
-                const uint32_t b = kPlanes ? b0 + plane_b(i) * kOperand : b0;
+            for (int kb = 0; ok && kb < blocks; ++kb, ++n_loads) {
+              const int s0 = n_loads % kDepth * kOps;
+              const uint32_t parity = (n_loads / kDepth) & 1;
+              // product of plane za of A and zb of B into the accumulator
+              auto product = [&](int za, int zb, uint32_t accumulate) {
+                const uint32_t a = smem_u32(smem + (s0 + za) * kSlotBytes);
+                const uint32_t b = smem_u32(smem + (s0 + zb) * kSlotBytes + kOperand);
 #pragma unroll
                 for (int k = 0; k < kBlockK / 16; ++k) {
                   const uint32_t ak = a + k * a_step, bk = b + k * b_step;
                   mma_bf16_ss_pair(d, g.a_mn ? sdesc_mn(ak) : sdesc_kmajor_sw128(ak),
                                    g.b_mn ? sdesc_mn(bk) : sdesc_kmajor_sw128(bk), idesc,
-                                   kb > 0 || i > 0 || k > 0);
+                                   accumulate | (uint32_t)(k > 0));
                 }
+                issued = true;
+              };
+              ok = mbar_wait(&full[s0], parity, abort_flag);
+              if constexpr (kPlanes) {
+                ok = ok && mbar_wait(&full[s0 + 2], parity, abort_flag);
+                if (!ok) break;
+                tc_fence_after_sync();
+                product(0, 2, kb > 0);
+                product(2, 0, 1);
+                mma_commit_pair(&empty[s0 + 2]);
+                ok = mbar_wait(&full[s0 + 1], parity, abort_flag);
+                if (!ok) break;
+                tc_fence_after_sync();
+                product(1, 1, 1);
+                product(0, 1, 1);
+                product(1, 0, 1);
+                mma_commit_pair(&empty[s0 + 1]);
+                product(0, 0, 1);
+              } else {
+                if (!ok) break;
+                tc_fence_after_sync();
+                product(0, 0, kb > 0);
               }
-              issued = true;
-              mma_commit_pair(&empty[s]);
+              mma_commit_pair(&empty[s0]);
             }
             if (ok) mma_commit_pair(&t_full[buf]);
           }
@@ -620,7 +629,7 @@ int pairs_of_device() { return std::max(1, sm_count() / 2); }
 // (16 KB of A, half the columns of B, of each plane) comes at some 48 bytes a
 // cycle.
 double block_cycles(int width, bool planes) {
-  return planes ? std::max(2.0 * kProducts * width, 3 * (341 + 1.33 * width))
+  return planes ? std::max(2.0 * 6 * width, 3 * (341 + 1.33 * width))
                 : std::max(2.0 * width, 341 + 1.33 * width);
 }
 constexpr double kTileCycles = 3000;  // to fill and empty the pipeline
