@@ -130,6 +130,12 @@ cudaError_t launch_key_sort(long long n, int K, const void* keys, bool keys64, i
                             int32_t* undo, int32_t* offsets, int32_t* sorted, int2* runs,
                             int32_t* zeros, int n_zeros, void* scratch, cudaStream_t st);
 
+// The same for two classes: entries whose key lies in [0, range) first, then
+// the others; offsets [2], offsets[1] the count of the former.  Scratch as for
+// one key.
+cudaError_t launch_row_order(long long n, int range, const void* keys, bool keys64, int32_t* perm,
+                             int32_t* undo, int32_t* offsets, void* scratch, cudaStream_t st);
+
 // ---- the token table: lookup, its gradient, cross entropy -----------------------
 // Validated copy of lsh_table.
 struct TableProblem {

@@ -72,6 +72,18 @@ struct RawKeys {
   __device__ int entry(int e) const { return e; }
 };
 
+// Key 0 where the entry's own key lies in [0, range), 1 outside.
+template <typename I>
+struct InRange {
+  const I* keys;
+  int range;
+  __device__ int key(int e) const {
+    const I k = keys[e];
+    return k >= 0 && k < (I)range ? 0 : 1;
+  }
+  __device__ int entry(int e) const { return e; }
+};
+
 struct OrderedKeys {
   const int32_t* keys;
   const int32_t* entries;
@@ -393,6 +405,21 @@ cudaError_t launch_key_sort(long long n_, int K, const void* keys, bool keys64, 
     note_launch();
   }
   return cudaSuccess;
+}
+
+cudaError_t launch_row_order(long long n, int range, const void* keys, bool keys64, int32_t* perm,
+                             int32_t* undo, int32_t* offsets, void* scratch, cudaStream_t st) {
+  const Plan p = make_plan(n, 1);
+  const Scratch s = scratch_layout(n, p);
+  char* base = static_cast<char*>(scratch);
+  int32_t* cnt = reinterpret_cast<int32_t*>(base + s.cnt);
+  int32_t* first = reinterpret_cast<int32_t*>(base + s.base);
+  const InRange<int64_t> r64{static_cast<const int64_t*>(keys), range};
+  const InRange<int32_t> r32{static_cast<const int32_t*>(keys), range};
+  return keys64 ? one_pass(p, r64, cnt, first, offsets, perm, undo, nullptr, nullptr, 0, (int)n,
+                           p.bins_lo, p.lo, 0, st)
+                : one_pass(p, r32, cnt, first, offsets, perm, undo, nullptr, nullptr, 0, (int)n,
+                           p.bins_lo, p.lo, 0, st);
 }
 
 }  // namespace lsh

@@ -73,6 +73,11 @@ struct Params {
   const float* lse;
   const float* dloss;
   int v0, vocab;          // the piece's first word
+  // rows that have a target, counted on the device (backward): slot s of the
+  // first *count holds row order[s]
+  const int32_t* count;
+  const int32_t* order;
+  bool count_k;           // the count bounds K, not D's rows
 };
 
 struct Item {
@@ -171,7 +176,7 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
   uint64_t* done = t_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
-  const Gemm& g = p.g;
+  Gemm g = p.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_ctarank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
@@ -195,6 +200,17 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
   tc_fence_after_sync();
   const uint32_t tmem = *tmem_slot;
   wait_prior_grid();
+  if (p.count) {
+    const int count = *p.count;
+    if (p.count_k) {
+      g.kb = (count + kBlockK - 1) / kBlockK;
+      g.kb_split = (g.kb + g.splits - 1) / g.splits;
+    } else {
+      g.rows = count;
+      g.m_tiles = (count + kTileM - 1) / kTileM;
+      g.items = g.m_tiles * g.slices * g.splits;
+    }
+  }
 
   if (warp == 0) {
     // -------------------------------------------------------------- loads
@@ -349,10 +365,12 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
       if (lane == 0) bulk_wait_read();
       __syncwarp();
     };
+    // g is written up to the end of the K block that holds its last row
+    const int row_end = kEpi == Epi::kGrad ? (g.rows + kBlockK - 1) / kBlockK * kBlockK : g.rows;
     auto send = [&](int x, int y, int plane) {
       fence_proxy_async_smem();
       __syncwarp();
-      if (lane == 0 && x < g.cols && y < g.rows) {
+      if (lane == 0 && x < g.cols && y < row_end && y < p.g.rows) {
         if constexpr (kEpi == Epi::kAdd) tma_add_3d(&omap, mine, x, y, plane);
         else tma_store_3d(&omap, mine, x, y, plane);
         bulk_commit();
@@ -393,10 +411,13 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
       float run_m = -INFINITY, run_s = 0.f, up = 0.f, lse2 = 0.f;
       if constexpr (kEpi == Epi::kLse || kEpi == Epi::kGrad) {
         if (row < g.rows) {
-          target = target_of(targets, row, p.vocab);
           if constexpr (kEpi == Epi::kGrad) {
-            up = target >= 0 ? p.dloss[row] * p.scale : 0.f;
-            lse2 = p.lse[row] * kLog2e;
+            const int at = p.order[row];
+            target = target_of(targets, at, p.vocab);
+            up = p.dloss[at] * p.scale;
+            lse2 = p.lse[at] * kLog2e;
+          } else {
+            target = target_of(targets, row, p.vocab);
           }
         }
       }
@@ -455,7 +476,7 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
             z[i] = e.x;
             z[i + 1] = e.y;
           }
-          // a row without a target takes no part, whatever its logits are
+          // slots past the last row hold zeros, whatever their logits are
           if (!all_there && target < 0) {
 #pragma unroll
             for (int i = 0; i < 32; ++i) z[i] = 0.f;
@@ -494,6 +515,15 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
         // this warp's 32-column chunks: halves of the groups half, half + 2
         const int chunks = groups > half + 2 ? 4 : groups > half ? 2 : 0;
         auto chunk_col = [&](int i) { return (half + (i & 2)) * 64 + (i & 1) * 32; };
+        if (it.k0 >= it.k1) {  // no rows in this part of K
+          float z[32];
+          for (int i = 0; i < chunks; ++i) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) z[j] = 0.f;
+            take(z, i & 1, col0 + chunk_col(i));
+          }
+          continue;
+        }
         if constexpr (!kPlanes) {
           const int buf = tile & 1;
           if (!mbar_wait(&t_full[buf], (tile >> 1) & 1, abort_flag)) { ok = false; break; }
@@ -576,20 +606,9 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
 }
 
 // ---------------------------------------------------------------- preparation
-// planes[3][rows][d]: three bfloat16 values whose sum is the float32 value to
-// 24 bits; zeros in rows without a target when `targets` is given.
-template <typename I>
-__global__ void __launch_bounds__(256)
-xent_planes_kernel(const float* __restrict__ src, const I* __restrict__ targets,
-                   __nv_bfloat16* __restrict__ planes, long long pieces, int per_row, int vocab) {
-  wait_prior_grid();
-  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-  if (i >= pieces) return;
-  float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (!targets || target_of(targets, i / per_row, vocab) >= 0) {
-    Vec16<float>::load(src + i * 8, f);
-    Vec16<float>::load(src + i * 8 + 4, f + 4);
-  }
+// Eight values to the three planes of piece i of `pieces`.
+__device__ __forceinline__ void put_planes(__nv_bfloat16* planes, long long pieces, long long i,
+                                           float* f) {
 #pragma unroll
   for (int pl = 0; pl < 3; ++pl) {
     Vec16<__nv_bfloat16>::store(planes + ((size_t)pl * pieces + i) * 8, f);
@@ -598,22 +617,79 @@ xent_planes_kernel(const float* __restrict__ src, const I* __restrict__ targets,
   }
 }
 
-// out = the sum of the planes, in their order.
-template <typename T>
+__device__ __forceinline__ void load8(const float* p, float* f) {
+  Vec16<float>::load(p, f);
+  Vec16<float>::load(p + 4, f + 4);
+}
+__device__ __forceinline__ void load8(const __nv_bfloat16* p, float* f) {
+  Vec16<__nv_bfloat16>::load(p, f);
+}
+
+// planes[3][rows][d]: three bfloat16 values whose sum is the float32 value to
+// 24 bits.
 __global__ void __launch_bounds__(256)
-xent_sum_kernel(const float* __restrict__ sums, T* __restrict__ out, long long pieces, int planes) {
+xent_planes_kernel(const float* __restrict__ src, __nv_bfloat16* __restrict__ planes,
+                   long long pieces) {
   wait_prior_grid();
   const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  if (i >= pieces) return;
+  float f[8];
+  load8(src + i * 8, f);
+  put_planes(planes, pieces, i, f);
+}
+
+// The rows of x that have a target, in their order (float32 ones as planes),
+// and zeros up to the end of the last K block.
+template <typename T>
+__global__ void __launch_bounds__(256)
+xent_rows_kernel(const T* __restrict__ x, const int32_t* __restrict__ order,
+                 const int32_t* __restrict__ count, __nv_bfloat16* __restrict__ rows,
+                 long long pieces, int per_row) {
+  wait_prior_grid();
+  const int n = *count, end = (n + kBlockK - 1) / kBlockK * kBlockK;
+  const PieceBlock at(blockIdx.x, 256, per_row);
+  long long slot;
+  int piece;
+  at.locate(threadIdx.x, per_row, &slot, &piece);
+  const long long i = at.first + threadIdx.x;
+  if (i >= pieces || slot >= end) return;
+  const T* from = x + ((size_t)(slot < n ? order[slot] : 0) * per_row + piece) * 8;
+  if constexpr (sizeof(T) == 2) {
+    *reinterpret_cast<uint4*>(rows + i * 8) =
+        slot < n ? Vec16<T>::raw(from) : make_uint4(0, 0, 0, 0);
+  } else {
+    float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (slot < n) load8(from, f);
+    put_planes(rows, pieces, i, f);
+  }
+}
+
+// out = the sum of the planes, in their order; with `slots`, row r of out is
+// row slots[r] of the planes, or zeros where that is not below *count.
+template <typename TS, typename T>
+__global__ void __launch_bounds__(256)
+xent_sum_kernel(const TS* __restrict__ sums, T* __restrict__ out,
+                const int32_t* __restrict__ slots, const int32_t* __restrict__ count,
+                long long pieces, int per_row, int planes) {
+  wait_prior_grid();
+  const PieceBlock at(blockIdx.x, 256, per_row);
+  long long row;
+  int piece;
+  at.locate(threadIdx.x, per_row, &row, &piece);
+  const long long i = at.first + threadIdx.x;
   if (i >= pieces) return;
   float a[8];
 #pragma unroll
   for (int t = 0; t < 8; ++t) a[t] = 0.f;
-  for (int s = 0; s < planes; ++s) {
-    float f[8];
-    Vec16<float>::load(sums + ((size_t)s * pieces + i) * 8, f);
-    Vec16<float>::load(sums + ((size_t)s * pieces + i) * 8 + 4, f + 4);
+  const long long slot = slots ? slots[row] : row;
+  if (!slots || slot < *count) {
+    const long long from = slot * per_row + piece;
+    for (int s = 0; s < planes; ++s) {
+      float f[8];
+      load8(sums + ((size_t)s * pieces + from) * 8, f);
 #pragma unroll
-    for (int t = 0; t < 8; ++t) a[t] += f[t];
+      for (int t = 0; t < 8; ++t) a[t] += f[t];
+    }
   }
 #pragma unroll
   for (int t = 0; t < 8; t += Vec16<T>::N) Vec16<T>::store(out + i * 8 + t, a + t);
@@ -637,8 +713,9 @@ constexpr double kTileCycles = 3000;  // to fill and empty the pipeline
 // K blocks per accumulator.  The tensor core truncates when it adds to one, an
 // error that grows with the number of additions to a sum of full size (1.1e-5
 // of dx after 500 of them): float32 operands get a new accumulator after
-// kPlaneChunk blocks, 28 such additions.
-constexpr int kPlaneChunk = 2;
+// kPlaneChunk blocks, 76 such additions (2047 x 8009 x 520, loss and gradients:
+// 2 blocks 426 us, 4 401, 16 390).
+constexpr int kPlaneChunk = 4;
 void set_chunk(Gemm* g) { g->chunk = g->planes ? kPlaneChunk : g->kb_split; }
 
 // Cuts D's columns into tiles (of a multiple of 64) and K into parts (with
@@ -716,9 +793,9 @@ constexpr size_t kGradBytes = 640u << 20;
 struct Backward {
   int words, pieces;
   size_t ld;             // columns of g
-  bool sum_dx, sum_dw;   // float32 sums outside the results
+  bool f32_dx, sum_dw;   // dx's rows in float32; dW's sums outside the result
   Gemm dx, dw;           // of a whole piece
-  size_t clean, w_planes, g, dx_sums, dw_sums, total;
+  size_t order, slots, count, rows, w_planes, g, dx_rows, dw_sums, sort, total;
 };
 
 Backward plan_backward(const TableProblem& p) {
@@ -743,16 +820,19 @@ Backward plan_backward(const TableProblem& p) {
   const int words = std::min(b.words, p.vocab);
   b.dx = make_gemm(p.rows, p.d, words, !p.bf16, false, true, true);
   b.dw = make_gemm(words, p.d, (int)p.rows, !p.bf16, true, true, true);
-  // with float32 results and no split K the result itself is the sum
-  b.sum_dx = b.dx.splits > 1 || (b.pieces > 1 && p.bf16);
+  b.f32_dx = !p.bf16 || b.dx.splits > 1 || b.pieces > 1;
   b.sum_dw = b.dw.splits > 1;
-  const size_t nd = (size_t)p.rows * p.d, vd = (size_t)b.words * p.d;
+  const size_t n = (size_t)p.rows, nd = n * p.d, vd = (size_t)b.words * p.d;
   size_t off = 0;
-  b.clean = off;    off += align256(nd * 2 * planes);
+  b.order = off;    off += align256(n * 4);
+  b.slots = off;    off += align256(n * 4);
+  b.count = off;    off += 256;
+  b.rows = off;     off += align256(nd * 2 * planes);
   b.w_planes = off; off += p.bf16 ? 0 : align256((size_t)p.vocab * p.d * 6);
-  b.g = off;        off += align256((size_t)planes * p.rows * b.ld * 2);
-  b.dx_sums = off;  off += b.sum_dx ? align256(nd * 4 * b.dx.splits) : 0;
+  b.g = off;        off += align256((size_t)planes * n * b.ld * 2);
+  b.dx_rows = off;  off += align256(nd * (b.f32_dx ? 4 : 2) * b.dx.splits);
   b.dw_sums = off;  off += b.sum_dw ? align256(vd * 4 * b.dw.splits) : 0;
+  b.sort = off;     off += key_sort_scratch_bytes(p.rows, 1);
   b.total = off;
   return b;
 }
@@ -797,29 +877,39 @@ cudaError_t launch_logits(bool idx64, const CUtensorMap& a, const CUtensorMap& b
                : launch<kEpi, float, int32_t, true>(a, b, o, p, st);
 }
 
-cudaError_t launch_planes(const TableProblem& p, const void* src, long long rows,
-                          const void* targets, void* planes, cudaStream_t st) {
-  const long long pieces = rows * (p.d / 8);
-  const dim3 grid((unsigned)((pieces + 255) / 256)), block(256);
-  __nv_bfloat16* to = static_cast<__nv_bfloat16*>(planes);
-  const float* from = static_cast<const float*>(src);
-  cudaError_t e =
-      p.idx64 ? launch_dependent(xent_planes_kernel<int64_t>, grid, block, 0, st, from,
-                                 static_cast<const int64_t*>(targets), to, pieces, p.d / 8, p.vocab)
-              : launch_dependent(xent_planes_kernel<int32_t>, grid, block, 0, st, from,
-                                 static_cast<const int32_t*>(targets), to, pieces, p.d / 8, p.vocab);
+cudaError_t launch_planes(const void* src, long long values, void* planes, cudaStream_t st) {
+  const long long pieces = values / 8;
+  cudaError_t e = launch_dependent(xent_planes_kernel, dim3((unsigned)((pieces + 255) / 256)),
+                                   dim3(256), 0, st, static_cast<const float*>(src),
+                                   static_cast<__nv_bfloat16*>(planes), pieces);
   if (e == cudaSuccess) note_launch();
   return e;
 }
 
-cudaError_t launch_sum(bool bf16, const float* sums, void* out, long long values, int planes,
-                       cudaStream_t st) {
-  const long long pieces = values / 8;
+cudaError_t launch_rows(const TableProblem& p, const void* x, const int32_t* order,
+                        const int32_t* count, void* rows, cudaStream_t st) {
+  const int per_row = p.d / 8;
+  const long long pieces = p.rows * per_row;
   const dim3 grid((unsigned)((pieces + 255) / 256)), block(256);
-  cudaError_t e = bf16 ? launch_dependent(xent_sum_kernel<__nv_bfloat16>, grid, block, 0, st, sums,
-                                          static_cast<__nv_bfloat16*>(out), pieces, planes)
-                       : launch_dependent(xent_sum_kernel<float>, grid, block, 0, st, sums,
-                                          static_cast<float*>(out), pieces, planes);
+  __nv_bfloat16* to = static_cast<__nv_bfloat16*>(rows);
+  cudaError_t e =
+      p.bf16 ? launch_dependent(xent_rows_kernel<__nv_bfloat16>, grid, block, 0, st,
+                                static_cast<const __nv_bfloat16*>(x), order, count, to, pieces, per_row)
+             : launch_dependent(xent_rows_kernel<float>, grid, block, 0, st,
+                                static_cast<const float*>(x), order, count, to, pieces, per_row);
+  if (e == cudaSuccess) note_launch();
+  return e;
+}
+
+// slots and count: see xent_sum_kernel.
+template <typename TS, typename T>
+cudaError_t launch_sum(const void* sums, void* out, const int32_t* slots, const int32_t* count,
+                       long long rows, int d, int planes, cudaStream_t st) {
+  const int per_row = d / 8;
+  const long long pieces = rows * per_row;
+  cudaError_t e = launch_dependent(xent_sum_kernel<TS, T>, dim3((unsigned)((pieces + 255) / 256)),
+                                   dim3(256), 0, st, static_cast<const TS*>(sums),
+                                   static_cast<T*>(out), slots, count, pieces, per_row, planes);
   if (e == cudaSuccess) note_launch();
   return e;
 }
@@ -827,14 +917,16 @@ cudaError_t launch_sum(bool bf16, const float* sums, void* out, long long values
 // Product into rows [0, g.rows) of out: straight into the result (splits == 1)
 // or into g.splits planes of float32 sums; `add` to what is there.
 cudaError_t launch_product(const Gemm& g, const CUtensorMap& a, const CUtensorMap& b, void* out,
-                           bool f32, int d, long long plane_rows, bool add, unsigned int* err,
-                           cudaStream_t st) {
+                           bool f32, int d, long long plane_rows, bool add, const int32_t* count,
+                           bool count_k, unsigned int* err, cudaStream_t st) {
   CUtensorMap o;
   if (!encode(&o, out, f32, d, g.rows, g.splits, d, plane_rows, f32 ? 32 : 64, 32))
     return cudaErrorInvalidValue;
   Params p = {};
   p.g = g;
   p.err = err;
+  p.count = count;
+  p.count_k = count_k;
   if (!f32) return launch<Epi::kStore, __nv_bfloat16, int32_t, false>(a, b, o, p, st);
   if (!g.planes)
     return add ? launch<Epi::kAdd, float, int32_t, false>(a, b, o, p, st)
@@ -864,8 +956,8 @@ cudaError_t launch_xent_tc(const TableProblem& p, const void* x, const void* tab
   if (!p.bf16) {
     void* xp = scratch;
     void* wp = static_cast<char*>(scratch) + align256((size_t)p.rows * p.d * 6);
-    if ((e = launch_planes(p, x, p.rows, nullptr, xp, st))) return e;
-    if ((e = launch_planes(p, table, p.vocab, nullptr, wp, st))) return e;
+    if ((e = launch_planes(x, p.rows * p.d, xp, st))) return e;
+    if ((e = launch_planes(table, (long long)p.vocab * p.d, wp, st))) return e;
     x = xp;
     table = wp;
   }
@@ -897,21 +989,27 @@ cudaError_t launch_xent_tc_backward(const TableProblem& p, const void* x, const 
   unsigned int* err = device_error_word();
   if (!err) return cudaErrorUnknown;
   cudaError_t e;
-  void* clean = ws + plan.clean;
+  int32_t* order = reinterpret_cast<int32_t*>(ws + plan.order);
+  int32_t* slots = reinterpret_cast<int32_t*>(ws + plan.slots);
+  int32_t* offsets = reinterpret_cast<int32_t*>(ws + plan.count);
+  const int32_t* count = offsets + 1;
+  void* rows = ws + plan.rows;
   const void* w = table;
+  // the rows that have a target, side by side
+  if ((e = launch_row_order(p.rows, p.vocab, targets, p.idx64, order, slots, offsets,
+                            ws + plan.sort, st)))
+    return e;
+  if ((e = launch_rows(p, x, order, count, rows, st))) return e;
   if (f32) {
-    if ((e = launch_planes(p, x, p.rows, targets, clean, st))) return e;
-    if ((e = launch_planes(p, table, p.vocab, nullptr, ws + plan.w_planes, st))) return e;
+    if ((e = launch_planes(table, (long long)p.vocab * p.d, ws + plan.w_planes, st))) return e;
     w = ws + plan.w_planes;
-  } else {
-    if ((e = launch_xent_clean(p, x, targets, clean, st))) return e;
   }
   void* gbuf = ws + plan.g;
-  float* dx_sums = reinterpret_cast<float*>(ws + plan.dx_sums);
-  float* dw_sums = reinterpret_cast<float*>(ws + plan.dw_sums);
+  void* dx_rows = ws + plan.dx_rows;
+  void* dw_sums = ws + plan.dw_sums;
   CUtensorMap x_k, x_mn, w_k, w_mn, g_k, g_mn, g_out;
-  if (!encode(&x_k, clean, false, p.d, p.rows, planes, p.d, p.rows, kBlockK, 128) ||
-      !encode(&x_mn, clean, false, p.d, p.rows, planes, p.d, p.rows, 64, kBlockK))
+  if (!encode(&x_k, rows, false, p.d, p.rows, planes, p.d, p.rows, kBlockK, 128) ||
+      !encode(&x_mn, rows, false, p.d, p.rows, planes, p.d, p.rows, 64, kBlockK))
     return cudaErrorInvalidValue;
   for (int v0 = 0; v0 < p.vocab; v0 += plan.words) {
     const int nv = std::min(plan.words, p.vocab - v0);
@@ -924,6 +1022,8 @@ cudaError_t launch_xent_tc_backward(const TableProblem& p, const void* x, const 
     k.scale = p.scale;
     k.lse = lse;
     k.dloss = dloss;
+    k.count = count;
+    k.order = order;
     k.v0 = v0;
     k.vocab = p.vocab;
     // (a piece sees its own words only: rows past them read as zeros)
@@ -943,8 +1043,8 @@ cudaError_t launch_xent_tc_backward(const TableProblem& p, const void* x, const 
     gx.splits = ceil_div(gx.kb, gx.kb_split);
     gx.items = gx.m_tiles * gx.n_tiles * gx.splits;
     set_chunk(&gx);
-    void* dx_to = plan.sum_dx ? static_cast<void*>(dx_sums) : dx;
-    if ((e = launch_product(gx, g_k, w_mn, dx_to, f32 || plan.sum_dx, p.d, p.rows, v0 > 0, err, st)))
+    if ((e = launch_product(gx, g_k, w_mn, dx_rows, plan.f32_dx, p.d, p.rows, v0 > 0, count, false,
+                            err, st)))
       return e;
     // dW = g^T x
     Gemm gw = plan.dw;
@@ -952,16 +1052,23 @@ cudaError_t launch_xent_tc_backward(const TableProblem& p, const void* x, const 
     gw.m_tiles = ceil_div(nv, kTileM);
     gw.items = gw.m_tiles * gw.n_tiles * gw.splits;
     char* dw_at = static_cast<char*>(dtable) + (size_t)v0 * p.d * p.elem();
-    void* dw_to = plan.sum_dw ? static_cast<void*>(dw_sums) : dw_at;
-    if ((e = launch_product(gw, g_mn, x_mn, dw_to, f32 || plan.sum_dw, p.d, nv, false, err, st)))
+    void* dw_to = plan.sum_dw ? dw_sums : dw_at;
+    if ((e = launch_product(gw, g_mn, x_mn, dw_to, f32 || plan.sum_dw, p.d, nv, false, count, true,
+                            err, st)))
       return e;
-    if (plan.sum_dw &&
-        (e = launch_sum(p.bf16, dw_sums, dw_at, (long long)nv * p.d, gw.splits, st)))
-      return e;
+    if (plan.sum_dw) {
+      e = f32 ? launch_sum<float, float>(dw_sums, dw_at, nullptr, nullptr, nv, p.d, gw.splits, st)
+              : launch_sum<float, __nv_bfloat16>(dw_sums, dw_at, nullptr, nullptr, nv, p.d,
+                                                 gw.splits, st);
+      if (e) return e;
+    }
   }
-  if (plan.sum_dx)
-    return launch_sum(p.bf16, dx_sums, dx, p.rows * p.d, plan.dx.splits, st);
-  return cudaSuccess;
+  // dx's rows to their places
+  if (f32) return launch_sum<float, float>(dx_rows, dx, slots, count, p.rows, p.d, plan.dx.splits, st);
+  if (plan.f32_dx)
+    return launch_sum<float, __nv_bfloat16>(dx_rows, dx, slots, count, p.rows, p.d, plan.dx.splits,
+                                            st);
+  return launch_sum<__nv_bfloat16, __nv_bfloat16>(dx_rows, dx, slots, count, p.rows, p.d, 1, st);
 }
 
 }  // namespace lsh

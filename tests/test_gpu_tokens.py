@@ -158,6 +158,25 @@ def test_xent(n, vocab, d, dtype, index, scale, holes, portable):
     assert torch.equal(again[0], dx) and torch.equal(again[1], dw)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("valid", [0, 1, 31, 32, 63, 64, 65, 97, 128, 255, 256, 257, 449, 600])
+def test_xent_backward_of_as_many_rows(valid, dtype):
+    # the rows with a target are gathered; what lies behind them is not read
+    x, table, t, dloss = make_xent(600, 333, 72, dtype, torch.int64, 0)
+    keep = torch.randperm(600, device=DEV, generator=gen(valid))[:valid]
+    targets = torch.full_like(t, -1)
+    targets[keep] = t[keep]
+    loss, lse = lsh.lsh_attn_xent(x, table, targets)
+    need = lsh.lsh_attn_xent_backward_workspace_size(
+        lsh.make_table_shape(600, 333, 72, dtype))
+    ws = torch.full((need,), 0xff, dtype=torch.uint8, device=DEV)    # NaN everywhere
+    dx, dw = lsh.lsh_attn_xent_backward(x, table, targets, lse, dloss, workspace=ws)
+    want_dx, want_dw = R.xent_backward(x, table, targets, dloss, 1.0,
+                                       BF16 if dtype == BF16 else None)
+    R.check("dx", dx, want_dx)
+    R.check("dtable", dw, want_dw)
+
+
 @pytest.mark.parametrize("n,vocab,d,dtype", [(20011, 14001, 24, BF16), (9001, 10007, 40, F32)])
 def test_xent_backward_in_pieces(n, vocab, d, dtype):
     # more gradient values than one piece of the vocabulary holds
