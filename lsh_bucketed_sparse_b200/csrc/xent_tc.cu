@@ -713,9 +713,10 @@ constexpr double kTileCycles = 3000;  // to fill and empty the pipeline
 // K blocks per accumulator.  The tensor core truncates when it adds to one, an
 // error that grows with the number of additions to a sum of full size (1.1e-5
 // of dx after 500 of them): float32 operands get a new accumulator after
-// kPlaneChunk blocks, 76 such additions (2047 x 8009 x 520, loss and gradients:
-// 2 blocks 426 us, 4 401, 16 390).
-constexpr int kPlaneChunk = 4;
+// kPlaneChunk blocks, 28 such additions: 6.5e-7 of dx and of dW, which sums in
+// float32 do not better.  (2047 x 8009 x 520, loss and gradients: 2 blocks 426
+// us, 4 401, 16 390; with 4 dW is further off than that, 1.5e-6.)
+constexpr int kPlaneChunk = 2;
 void set_chunk(Gemm* g) { g->chunk = g->planes ? kPlaneChunk : g->kb_split; }
 
 // Cuts D's columns into tiles (of a multiple of 64) and K into parts (with
