@@ -537,12 +537,12 @@ def _workspace(workspace, need, like):
         return workspace, workspace.numel()
     if need == 0:
         return None, 0
-    return torch.empty(need, dtype=torch.uint8, device=like.device), need
+    return like.new_empty(need, dtype=torch.uint8), need
 
 
 def _out(t, name, dtype, shape, like):
     if t is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return like.new_empty(shape, dtype=dtype)
     return _cuda(t, name, dtype, shape, like)
 
 
@@ -620,8 +620,7 @@ def lsh_attn_xent(x, table, targets, *, scale=1.0, workspace=None, portable=Fals
     shp = _xent_args(x, table, targets, scale, portable)
     need = lsh_attn_xent_workspace_size(shp)
     with _launching(x.device, stream) as st:
-        loss = _out(None, "loss", torch.float32, targets.shape, x)
-        lse = _out(None, "lse", torch.float32, targets.shape, x)
+        loss, lse = x.new_empty((2, *targets.shape), dtype=torch.float32).unbind(0)
         ws, n = _workspace(workspace, need, x)
         _check(lib().lsh_attn_xent(ctypes.byref(shp), x.data_ptr(), table.data_ptr(), targets.data_ptr(),
                                    loss.data_ptr(), lse.data_ptr(), (None if ws is None else ws.data_ptr()), n, st))
@@ -641,8 +640,7 @@ def lsh_attn_xent_backward(x, table, targets, lse, dloss, *, scale=1.0, workspac
     _cuda(dloss, "dloss", torch.float32, targets.shape, x)
     need = lsh_attn_xent_backward_workspace_size(shp)
     with _launching(x.device, stream) as st:
-        dx = _out(None, "dx", x.dtype, x.shape, x)
-        dtable = _out(None, "dtable", x.dtype, table.shape, x)
+        dx, dtable = torch.empty_like(x), torch.empty_like(table)
         ws, n = _workspace(workspace, need, x)
         _check(lib().lsh_attn_xent_backward(ctypes.byref(shp), x.data_ptr(), table.data_ptr(),
                                             targets.data_ptr(), lse.data_ptr(), dloss.data_ptr(), dx.data_ptr(),
@@ -667,9 +665,9 @@ def lsh_attn_route_sort(experts, n_experts, *, workspace=None, stream=None):
     shp = make_route_shape(T, k, n_experts, index_type=_index_code(experts, "experts"))
     need = lsh_attn_route_sort_workspace_size(shp)
     with _launching(experts.device, stream) as st:
-        perm = torch.empty(T * k, dtype=torch.int32, device=experts.device)
-        undo = torch.empty(T, k, dtype=torch.int32, device=experts.device)
-        offsets = torch.empty(n_experts + 1, dtype=torch.int32, device=experts.device)
+        perm = experts.new_empty(T * k, dtype=torch.int32)
+        undo = experts.new_empty((T, k), dtype=torch.int32)
+        offsets = experts.new_empty(n_experts + 1, dtype=torch.int32)
         ws, n = _workspace(workspace, need, experts)
         _check(lib().lsh_attn_route_sort(ctypes.byref(shp), experts.data_ptr(), perm.data_ptr(), undo.data_ptr(),
                                          offsets.data_ptr(), (None if ws is None else ws.data_ptr()), n, st))

@@ -20,6 +20,7 @@
 // in the same float32 accumulator, small ones first: the three left out are
 // below 2^-24 of the largest.
 #include <algorithm>
+#include <atomic>
 
 #include "common.cuh"
 #include "internal.h"
@@ -859,8 +860,16 @@ template <Epi kEpi, typename T, typename I, bool kPlanes>
 cudaError_t launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o,
                    const Params& p, cudaStream_t st) {
   auto kernel = xent_tc_kernel<kEpi, T, I, kPlanes>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  static std::atomic<unsigned long long> set{0};  // devices that know the size already
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+  if (!(set.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    if (e) return e;
+    set.fetch_or(bit, std::memory_order_relaxed);
+  }
   const int pairs = std::min(pairs_of_device(), p.g.items);
   e = launch_dependent(kernel, dim3(2 * pairs), dim3(kThreads), (size_t)kSmem, st, a, b, o, p);
   if (e == cudaSuccess) note_launch();
