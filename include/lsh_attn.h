@@ -498,6 +498,10 @@ LSH_ATTN_API unsigned long long lsh_attn_kernel_launches(void);
  * normal behaviour.  Process-wide; not for use while other threads launch. */
 LSH_ATTN_API unsigned long long lsh_attn_test_hash_first_wait(unsigned long long ns);
 
+/* The same for the tensor-core cross entropy: the MMA thread's first wait for
+ * operands of every launch of it. */
+LSH_ATTN_API unsigned long long lsh_attn_test_xent_first_wait(unsigned long long ns);
+
 #ifdef __cplusplus
 }
 #endif

@@ -122,6 +122,7 @@ _SIGS = {
     "lsh_attn_version": [],
     "lsh_attn_kernel_launches": [],
     "lsh_attn_test_hash_first_wait": [ctypes.c_ulonglong],
+    "lsh_attn_test_xent_first_wait": [ctypes.c_ulonglong],
 }
 
 
@@ -141,6 +142,7 @@ def lib() -> ctypes.CDLL:
         L.lsh_attn_last_error.restype = ctypes.c_char_p
         L.lsh_attn_kernel_launches.restype = ctypes.c_ulonglong
         L.lsh_attn_test_hash_first_wait.restype = ctypes.c_ulonglong
+        L.lsh_attn_test_xent_first_wait.restype = ctypes.c_ulonglong
         _lib = L
     return _lib
 

@@ -375,6 +375,12 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
                : "memory");
 }
 
+// Sets the int at this place to 1 in CTA `rank` of the cluster.
+__device__ __forceinline__ void raise_flag_cluster(const int* flag, uint32_t rank) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(cluster_addr(flag, rank)), "r"(1)
+               : "memory");
+}
+
 // A tile to this CTA's shared memory, counted on a barrier of either CTA of
 // the pair (address of the cluster).
 __device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map,

@@ -4,6 +4,7 @@
 
 #include "internal.h"
 #include "lsh_attn.h"
+#include "xent.cuh"
 
 namespace lsh {
 namespace {
@@ -263,6 +264,10 @@ lsh_status lsh_attn_route_combine_backward(const lsh_route* shape, const void* d
   return launched(launch_route_combine_backward(p, dout, y, weights, undo, offsets, dy, dweights,
                                                 static_cast<cudaStream_t>(stream)),
                   "route combine backward launch");
+}
+
+unsigned long long lsh_attn_test_xent_first_wait(unsigned long long ns) {
+  return set_xent_first_wait_ns(ns);
 }
 
 }  // extern "C"

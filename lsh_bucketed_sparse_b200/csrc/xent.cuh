@@ -36,6 +36,9 @@ cudaError_t launch_xent_clean(const TableProblem& p, const void* x, const void* 
 
 // ---- tensor cores (xent_tc.cu) ---------------------------------------------------
 bool xent_tc_supported(const TableProblem& p);
+// Sets the limit of the MMA thread's first wait (test hook); returns the
+// previous limit.
+unsigned long long set_xent_first_wait_ns(unsigned long long ns);
 int xent_tc_slices(const TableProblem& p);
 size_t xent_tc_bytes(const TableProblem& p);  // of scratch
 cudaError_t launch_xent_tc(const TableProblem& p, const void* x, const void* table,

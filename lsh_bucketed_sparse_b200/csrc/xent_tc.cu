@@ -79,6 +79,7 @@ struct Params {
   const int32_t* count;
   const int32_t* order;
   bool count_k;           // the count bounds K, not D's rows
+  unsigned long long first_wait_ns;  // limit of the MMA thread's first wait for operands
 };
 
 struct Item {
@@ -177,6 +178,12 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
   uint64_t* done = t_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  // A wait ran out: every role of both CTAs leaves its loop.
+  auto give_up = [&](unsigned int code) {
+    atomicOr(p.err, code);
+    raise_flag_cluster(const_cast<int*>(abort_flag), 0);
+    raise_flag_cluster(const_cast<int*>(abort_flag), 1);
+  };
   Gemm g = p.g;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)cluster_ctarank();
@@ -260,19 +267,19 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
         }
       }
       if (!ok) {
-        atomicOr(p.err, kErrWaitProducer);
-        *abort_flag = 1;
+        give_up(kErrWaitProducer);
       }
       // The last loads must land before either CTA may exit (CTA 1 waits for
       // CTA 0 at the end).
-      if (rank == 0)
-        for (int l = n_loads > kDepth ? n_loads - kDepth : 0; l < n_loads; ++l)
-          for (int z = 0; z < kOps; ++z) {
-            const unsigned long long t0 = globaltimer();
-            while (!mbar_try_wait(&full[l % kDepth * kOps + z], (l / kDepth) & 1)) {
-              if (globaltimer() - t0 > kWaitLimitNs) { atomicOr(p.err, kErrWaitDrain); break; }
-            }
-          }
+      if (rank == 0) {
+        const unsigned long long t0 = globaltimer();
+        bool landed = true;
+        for (int l = n_loads > kDepth ? n_loads - kDepth : 0; landed && l < n_loads; ++l)
+          for (int z = 0; landed && z < kOps; ++z)
+            while (landed && !mbar_try_wait(&full[l % kDepth * kOps + z], (l / kDepth) & 1))
+              landed = globaltimer() - t0 <= kWaitLimitNs;
+        if (!landed) atomicOr(p.err, kErrWaitDrain);
+      }
     }
   } else if (warp == 1) {
     // -------------------------------------------------------------- MMAs
@@ -311,7 +318,8 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
                 }
                 issued = true;
               };
-              ok = mbar_wait(&full[s0], parity, abort_flag);
+              ok = mbar_wait_for(&full[s0], parity, abort_flag,
+                                 n_loads == 0 ? p.first_wait_ns : kWaitLimitNs);
               if constexpr (kPlanes) {
                 ok = ok && mbar_wait(&full[s0 + 2], parity, abort_flag);
                 if (!ok) break;
@@ -339,8 +347,7 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
         }
       }
       if (!ok) {
-        atomicOr(p.err, kErrWaitMma);
-        *abort_flag = 1;
+        give_up(kErrWaitMma);
       }
       if (issued) {  // every MMA finishes before tensor memory is released
         asm volatile(
@@ -594,10 +601,7 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
     if constexpr (kEpi != Epi::kLse) {
       if (lane == 0) bulk_wait();
     }
-    if (!ok) {
-      atomicOr(p.err, kErrWaitEpilogue);
-      *abort_flag = 1;
-    }
+    if (!ok) give_up(kErrWaitEpilogue);
   }
   __syncwarp();
   tc_fence_before_sync();
@@ -697,6 +701,10 @@ xent_sum_kernel(const TS* __restrict__ sums, T* __restrict__ out,
 }
 
 // ---------------------------------------------------------------- host side
+// Limit of the MMA thread's first wait (normally the 2 s of every bounded
+// wait); lsh_attn_test_xent_first_wait sets it to exercise the timeout path.
+std::atomic<unsigned long long> g_first_wait_ns{kWaitLimitNs};
+
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 int pairs_of_device() { return std::max(1, sm_count() / 2); }
@@ -871,7 +879,9 @@ cudaError_t launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap
     set.fetch_or(bit, std::memory_order_relaxed);
   }
   const int pairs = std::min(pairs_of_device(), p.g.items);
-  e = launch_dependent(kernel, dim3(2 * pairs), dim3(kThreads), (size_t)kSmem, st, a, b, o, p);
+  Params q = p;
+  q.first_wait_ns = g_first_wait_ns.load(std::memory_order_relaxed);
+  e = launch_dependent(kernel, dim3(2 * pairs), dim3(kThreads), (size_t)kSmem, st, a, b, o, q);
   if (e == cudaSuccess) note_launch();
   return e;
 }
@@ -946,6 +956,10 @@ cudaError_t launch_product(const Gemm& g, const CUtensorMap& a, const CUtensorMa
 }
 
 }  // namespace
+
+unsigned long long set_xent_first_wait_ns(unsigned long long ns) {
+  return g_first_wait_ns.exchange(ns);
+}
 
 bool xent_tc_supported(const TableProblem& p) {
   // (the limit keeps the count of tiles within 32 bits)

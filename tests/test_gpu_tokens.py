@@ -126,6 +126,11 @@ XENT = [  # rows, vocab, d, dtype, index, scale, holes
     (700, 5000, 64, BF16, torch.int64, 1.0, 0.05),
     (1025, 3001, 40, F32, torch.int64, 1.0, 0.1),
     (33, 20011, 24, BF16, torch.int64, 1.0, 0),
+    (40, 300, 64, BF16, torch.int64, 0.0, 0.1),     # every word as likely
+    (3, 70, 16384, BF16, torch.int64, 1.0, 0),
+    (3, 70, 16384, F32, torch.int32, 1.0, 0),
+    (9, 1 << 20, 16, BF16, torch.int64, 1.0, 0),
+    (2, 100003, 72, F32, torch.int64, 1.0, 0),
 ]
 
 
@@ -286,6 +291,48 @@ def test_xent_gradient_against_differences(portable):
     assert abs(slope - mine) <= bound
 
 
+def test_xent_of_any_leading_shape_and_a_slice_of_targets():
+    g = gen(21)
+    ids = torch.randint(0, 300, (2 * 7 * 5 + 1,), device=DEV, generator=g)
+    targets, x = ids[1:].view(2, 7, 5), randn(g, 2, 7, 5, 64, dtype=BF16)
+    table = randn(g, 300, 64, dtype=BF16)
+    loss, lse = lsh.lsh_attn_xent(x, table, targets)
+    assert loss.shape == lse.shape == targets.shape
+    flat = lsh.lsh_attn_xent(x.view(-1, 64), table, targets.reshape(-1).clone())
+    assert torch.equal(loss.view(-1), flat[0]) and torch.equal(lse.view(-1), flat[1])
+    up = torch.ones_like(loss)
+    dx, dw = lsh.lsh_attn_xent_backward(x, table, targets, lse, up)
+    want = lsh.lsh_attn_xent_backward(x.view(-1, 64), table, targets.reshape(-1).clone(),
+                                      flat[1], up.view(-1))
+    assert torch.equal(dx.view(-1, 64), want[0]) and torch.equal(dw, want[1])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_xent_wait_that_runs_out_reports_timeout_and_next_call_is_clean(dtype):
+    # the first wait gives up at once, before any product is issued: both CTAs
+    # of every pair leave their loops, and the context stays usable
+    x, table, t, dloss = make_xent(700, 900, 64, dtype, torch.int64, 0)
+    lib = lsh.lib()
+    lsh.lsh_attn_device_check()
+    prev = lib.lsh_attn_test_xent_first_wait(0)
+    try:
+        lsh.lsh_attn_xent(x, table, t)
+        with pytest.raises(lsh.LshError) as err:
+            lsh.lsh_attn_device_check()
+        assert err.value.status == 5  # LSH_ERR_DEVICE_TIMEOUT
+    finally:
+        assert lib.lsh_attn_test_xent_first_wait(prev) == 0
+    loss, lse = lsh.lsh_attn_xent(x, table, t)
+    dx, dw = lsh.lsh_attn_xent_backward(x, table, t, lse, dloss)
+    lsh.lsh_attn_device_check()
+    want_loss, want_lse = R.xent(x, table, t, 1.0)
+    R.check("lse", lse, want_lse)
+    R.check("loss", loss, want_loss)
+    want_dx, want_dw = R.xent_backward(x, table, t, dloss, 1.0, BF16 if dtype == BF16 else None)
+    R.check("dx", dx, want_dx)
+    R.check("dtable", dw, want_dw)
+
+
 # ---- routing ---------------------------------------------------------------------
 ROUTE = [  # tokens, k, experts, d, dtype, index, dropped
     (0, 2, 4, 16, BF16, torch.int64, 0),
@@ -391,6 +438,68 @@ def test_a_step_against_float64_autograd():
     for name, got, ref in (("loss", loss, want.detach()), ("dweights", dweights, w64.grad),
                            ("dtable", dtable, t64.grad)):
         err = float((got.detach().double() - ref).abs().max() / ref.abs().max())
+        assert err <= tol, f"{name}: {err:.3e} > {tol:.3e}"
+
+
+def test_a_language_model_step_through_the_attention():
+    """Token table, LSH attention in one chunk (so every position sees every
+    other: the definition is a dense softmax), routed copies, loss against the
+    same table, and the whole gradient, against float64 autograd."""
+    g = gen(31)
+    B, H, L, dk, V = 2, 2, 64, 16, 300
+    D = H * dk
+    tok = make_tokens(g, B * L, V, torch.int64, 0.1).view(B, L)
+    targets = torch.cat([tok[:, 1:], torch.full_like(tok[:, :1], -1)], dim=1)
+    table = randn(g, V, D, scale=D ** -0.5)
+    ids = make_tokens(g, B * L * 2, 5, torch.int64, 0, 0.1).view(B * L, 2)
+    w = torch.rand(B * L, 2, device=DEV, generator=g)
+
+    def heads(t):
+        return t.view(B, L, H, dk).transpose(1, 2).contiguous()
+
+    def rows(t):
+        return t.transpose(1, 2).reshape(B * L, D)
+
+    h = lsh.lsh_attn_embed(tok, table, scale=4.0)
+    qk = heads(h)
+    buckets, inv_norm = lsh.lsh_attn_hash(qk, None, 1)
+    perm, _, _ = lsh.lsh_attn_sort(buckets, 1)
+    out, lse_a = lsh.lsh_attn_forward(qk, qk, None, 1, 1, L, True)
+    a = rows(out).contiguous()
+    _, undo, off = lsh.lsh_attn_route_sort(ids, 5)
+    ys = lsh.lsh_attn_route_gather(a, undo, off)
+    x = lsh.lsh_attn_route_combine(ys, w, undo, off) + h.view(B * L, D)
+    loss, lse = lsh.lsh_attn_xent(x, table, targets.view(-1))
+    up = (targets.view(-1) >= 0).float() / (targets >= 0).sum()
+    dx, dtable = lsh.lsh_attn_xent_backward(x, table, targets.view(-1), lse, up)
+    dys, dw = lsh.lsh_attn_route_combine_backward(dx, ys, w, undo, off)
+    da = lsh.lsh_attn_route_gather_backward(dys, undo, off)
+    dqk, dv = lsh.lsh_attn_backward(qk, qk, inv_norm, perm, out, lse_a, heads(da), L, True,
+                                    n_buckets=1)
+    dh = dx + rows(dqk + dv)
+    lsh.lsh_attn_embed_backward(tok, dh.view(B, L, D), V, scale=4.0, init=dtable, out=dtable)
+    lsh.lsh_attn_device_check()
+
+    t64, w64 = table.double().requires_grad_(), w.double().requires_grad_()
+    h64 = 4.0 * t64[tok]
+    q = h64.view(B, L, H, dk).transpose(1, 2)
+    s = (q @ (q / q.norm(dim=-1, keepdim=True)).transpose(2, 3)) / math.sqrt(dk)
+    eye = torch.eye(L, device=DEV, dtype=torch.bool)
+    s = s.masked_fill(eye, -1e5).masked_fill(torch.ones_like(eye).triu(1), -math.inf)
+    a64 = (s.softmax(-1) @ q).transpose(1, 2).reshape(B * L, D)
+    kept = ((ids >= 0) & (ids < 5)).double()
+    x64 = (w64 * kept).sum(1, keepdim=True) * a64 + h64.view(B * L, D)
+    z = x64 @ t64.T
+    t = targets.view(-1)
+    want = torch.where(t >= 0, torch.logsumexp(z, 1) - z.gather(1, t.clamp(min=0)[:, None])[:, 0],
+                       0.0)
+    (want * up.double()).sum().backward()
+    # float32 throughout: eight steps of sums of up to V terms, each off by
+    # 2 * 300 * 2^-24 of magnitudes within 2^4 of the largest result
+    tol = 8 * 16 * 2 * 300 * 2.0 ** -24
+    for name, got, ref in (("loss", loss, want.detach()), ("dweights", dw, w64.grad),
+                           ("dtable", dtable, t64.grad)):
+        err = float((got.double() - ref).abs().max() / ref.abs().max())
         assert err <= tol, f"{name}: {err:.3e} > {tol:.3e}"
 
 
