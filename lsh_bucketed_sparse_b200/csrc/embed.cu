@@ -89,8 +89,8 @@ __device__ __forceinline__ void put_row(T* out, const float* a, float scale, boo
 template <typename T, bool kInit>
 __global__ void __launch_bounds__(kThreads, !kInit ? 4 : sizeof(T) == 4 ? 6 : 5)
 embed_grad_kernel(const int32_t* __restrict__ perm, const int32_t* __restrict__ sorted,
-                  const int2* __restrict__ runs, const T* __restrict__ dout, const T* init,
-                  T* dtable, float* part, int32_t* arrived, int n, int slot_blocks, int col_blocks,
+                  const int2* __restrict__ runs, const uint32_t* __restrict__ present,
+                  const T* __restrict__ dout, const T* init, T* dtable, float* part, int32_t* arrived, int n, int slot_blocks, int col_blocks,
                   int vocab, int d, int lanes, float scale) {
   using V = Vec16<T>;
   constexpr int kAhead = kInit ? 2 : 6;
@@ -102,19 +102,18 @@ embed_grad_kernel(const int32_t* __restrict__ perm, const int32_t* __restrict__ 
   if ((int)blockIdx.x >= slot_blocks * col_blocks) {
     const int per_row = d / V::N;
     const PieceBlock at(blockIdx.x - slot_blocks * col_blocks, kThreads * kPieces, per_row);
-    int2 run[kPieces];
-    const long long pieces = (long long)vocab * per_row;
+    bool empty[kPieces];
 #pragma unroll
     for (int u = 0; u < kPieces; ++u) {
       long long v;
       int col;
       at.locate(u * kThreads + threadIdx.x, per_row, &v, &col);
-      run[u] = v < vocab ? runs[v] : make_int2(0, 1);
+      empty[u] = v < vocab && !(present[v >> 5] >> (v & 31) & 1);
     }
 #pragma unroll
     for (int u = 0; u < kPieces; ++u) {
       const long long p = at.first + u * kThreads + threadIdx.x;
-      if (p >= pieces || run[u].x != run[u].y) continue;
+      if (!empty[u]) continue;
       uint4 old = make_uint4(0, 0, 0, 0);
       if (kInit) old = V::raw(init + p * V::N);
       *reinterpret_cast<uint4*>(dtable + p * V::N) = old;
@@ -263,15 +262,15 @@ Cut cut_of(const TableProblem& p) {
 
 template <typename T>
 cudaError_t grad_t(const TableProblem& p, const int32_t* perm, const int32_t* sorted,
-                   const int2* runs, const void* dout, const void* init, void* dtable, float* part,
-                   int32_t* arrived, const Cut& c, cudaStream_t st) {
+                   const int2* runs, const uint32_t* present, const void* dout, const void* init,
+                   void* dtable, float* part, int32_t* arrived, const Cut& c, cudaStream_t st) {
   // rows without a token: nothing to do where the gradient is added in place
   const long long pieces = init == dtable ? 0 : (long long)p.vocab * (p.d / Vec16<T>::N);
   const long long blocks = (long long)c.slot_blocks * c.col_blocks +
                            (pieces + kThreads * kPieces - 1) / (kThreads * kPieces);
   cudaError_t e = launch_dependent(init ? embed_grad_kernel<T, true> : embed_grad_kernel<T, false>,
                                    dim3((unsigned)blocks), dim3(kThreads), 0, st, perm, sorted,
-                                   runs, static_cast<const T*>(dout), static_cast<const T*>(init),
+                                   runs, present, static_cast<const T*>(dout), static_cast<const T*>(init),
                                    static_cast<T*>(dtable), part, arrived, (int)p.rows,
                                    c.slot_blocks, c.col_blocks, p.vocab, p.d, c.lanes, p.scale);
   if (e) return e;
@@ -322,7 +321,7 @@ cudaError_t embed_t(const TableProblem& p, const void* tokens, const void* table
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 struct Scratch {
-  size_t perm, sorted, runs, part, arrived, sort, total;
+  size_t perm, sorted, runs, present, part, arrived, sort, total;
   int n_arrived;  // counters, none where one block takes all slots
 };
 
@@ -337,6 +336,7 @@ Scratch scratch_layout(const TableProblem& p) {
   s.perm = off;    off += align256(n * sizeof(int32_t));
   s.sorted = off;  off += align256(n * sizeof(int32_t));
   s.runs = off;    off += align256((size_t)p.vocab * sizeof(int2));
+  s.present = off; off += align256((size_t)(p.vocab + 31) / 32 * sizeof(uint32_t));
   s.part = off;    off += joins ? align256((size_t)c.slot_blocks * 2 * p.d * sizeof(float)) : 0;
   s.arrived = off; off += align256((size_t)s.n_arrived * sizeof(int32_t));
   s.sort = off;    off += key_sort_scratch_bytes(p.rows, p.vocab);
@@ -372,15 +372,23 @@ cudaError_t launch_embed_backward(const TableProblem& p, const void* tokens, con
   int32_t* perm = reinterpret_cast<int32_t*>(base + s.perm);
   int32_t* sorted = reinterpret_cast<int32_t*>(base + s.sorted);
   int2* runs = reinterpret_cast<int2*>(base + s.runs);
+  uint32_t* present = reinterpret_cast<uint32_t*>(base + s.present);
   float* part = reinterpret_cast<float*>(base + s.part);
   int32_t* arrived = reinterpret_cast<int32_t*>(base + s.arrived);
-  cudaError_t e = launch_key_sort(p.rows, p.vocab, tokens, p.idx64, perm, nullptr, nullptr, sorted,
-                                  runs, arrived, s.n_arrived, base + s.sort, st);
+  KeyOrder o = {};
+  o.perm = perm;
+  o.sorted = sorted;
+  o.runs = runs;
+  o.present = present;
+  o.zeros = arrived;
+  o.n_zeros = s.n_arrived;
+  cudaError_t e = launch_key_sort(p.rows, p.vocab, tokens, p.idx64, o, base + s.sort, st);
   if (e) return e;
   const Cut c = cut_of(p);
-  return p.bf16 ? grad_t<__nv_bfloat16>(p, perm, sorted, runs, dout, init, dtable, part, arrived, c,
-                                        st)
-                : grad_t<float>(p, perm, sorted, runs, dout, init, dtable, part, arrived, c, st);
+  return p.bf16 ? grad_t<__nv_bfloat16>(p, perm, sorted, runs, present, dout, init, dtable, part,
+                                        arrived, c, st)
+                : grad_t<float>(p, perm, sorted, runs, present, dout, init, dtable, part, arrived, c,
+                                st);
 }
 
 }  // namespace lsh

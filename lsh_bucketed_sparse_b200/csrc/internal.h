@@ -120,21 +120,24 @@ cudaError_t launch_combine(const Problem& p, const void* o_rounds, const float* 
                            void* out, float* lse, cudaStream_t st);
 
 // ---- stable order of integer keys (key_sort.cu) -------------------------------
-// Keys outside [0, K) come last.  perm[s]: the entry in slot s; undo (may be
-// NULL) its inverse; offsets (may be NULL; K < 1024 only) [K + 1]: each key's
-// first slot, offsets[K] the first slot of the keys outside; with runs (may be
-// NULL), sorted[n] gets the keys in order and runs[K] each key's slots [x, y),
-// and zeros[0, n_zeros) is cleared (n_zeros <= n).
+// Keys outside [0, K) come last.  Any of the results may be NULL.
+struct KeyOrder {
+  int32_t* perm;      // [n] the entry in slot s
+  int32_t* undo;      // [n] its inverse
+  int32_t* offsets;   // [K + 1] each key's first slot, then the first of those outside; K < 1024 only
+  int32_t* sorted;    // [n] the key in slot s (K: outside)
+  int2* runs;         // [K] the slots [x, y) of each key that occurs (needs sorted and present)
+  uint32_t* present;  // [(K + 31) / 32] bit k: key k occurs
+  int32_t* zeros;     // cleared for a later kernel (with runs)
+  int n_zeros;        // at most n
+};
 size_t key_sort_scratch_bytes(long long n, int K);
-cudaError_t launch_key_sort(long long n, int K, const void* keys, bool keys64, int32_t* perm,
-                            int32_t* undo, int32_t* offsets, int32_t* sorted, int2* runs,
-                            int32_t* zeros, int n_zeros, void* scratch, cudaStream_t st);
-
-// The same for two classes: entries whose key lies in [0, range) first, then
-// the others; offsets [2], offsets[1] the count of the former.  Scratch as for
-// one key.
-cudaError_t launch_row_order(long long n, int range, const void* keys, bool keys64, int32_t* perm,
-                             int32_t* undo, int32_t* offsets, void* scratch, cudaStream_t st);
+cudaError_t launch_key_sort(long long n, int K, const void* keys, bool keys64, const KeyOrder& o,
+                            void* scratch, cudaStream_t st);
+// The same for two classes: entries whose key lies in [0, range) are key 0,
+// the others are outside (K = 1).
+cudaError_t launch_row_order(long long n, int range, const void* keys, bool keys64,
+                             const KeyOrder& o, void* scratch, cudaStream_t st);
 
 // ---- the token table: lookup, its gradient, cross entropy -----------------------
 // Validated copy of lsh_table.

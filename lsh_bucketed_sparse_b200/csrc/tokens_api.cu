@@ -206,8 +206,11 @@ lsh_status lsh_attn_route_sort(const lsh_route* shape, const void* experts, int3
   if (p.tokens == 0)
     return launched(cudaMemsetAsync(offsets, 0, (size_t)(p.experts + 1) * sizeof(int32_t), st),
                     "clear offsets");
-  return launched(launch_key_sort(p.entries(), p.experts, experts, p.idx64, perm, undo, offsets,
-                                  nullptr, nullptr, nullptr, 0, workspace, st),
+  KeyOrder o = {};
+  o.perm = perm;
+  o.undo = undo;
+  o.offsets = offsets;
+  return launched(launch_key_sort(p.entries(), p.experts, experts, p.idx64, o, workspace, st),
                   "route sort launch");
 }
 

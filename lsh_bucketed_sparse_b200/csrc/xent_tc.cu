@@ -1020,9 +1020,11 @@ cudaError_t launch_xent_tc_backward(const TableProblem& p, const void* x, const 
   void* rows = ws + plan.rows;
   const void* w = table;
   // the rows that have a target, side by side
-  if ((e = launch_row_order(p.rows, p.vocab, targets, p.idx64, order, slots, offsets,
-                            ws + plan.sort, st)))
-    return e;
+  KeyOrder o = {};
+  o.perm = order;
+  o.undo = slots;
+  o.offsets = offsets;
+  if ((e = launch_row_order(p.rows, p.vocab, targets, p.idx64, o, ws + plan.sort, st))) return e;
   if ((e = launch_rows(p, x, order, count, rows, st))) return e;
   if (f32) {
     if ((e = launch_planes(table, (long long)p.vocab * p.d, ws + plan.w_planes, st))) return e;

@@ -66,7 +66,10 @@ EMBED_BWD = [  # rows, vocab, d, dtype, index, skew, holes
     (20000, 300, 264, BF16, torch.int64, 0.9, 0),
     (300, 10, 16384, F32, torch.int64, 0.5, 0),
     (257, 3, 1032, BF16, torch.int64, 0.9, 0),
-    (65537, 200, 16, BF16, torch.int32, 0.2, 0.1),   # more than the small tiles take
+    (16384, 40000, 8, BF16, torch.int64, 0.1, 0.1),  # the most of a cluster
+    (16385, 1 << 20, 8, BF16, torch.int32, 0.1, 0.1),  # one more than it takes
+    (65537, 200, 16, BF16, torch.int32, 0.2, 0.1),
+    (70001, 40000, 8, F32, torch.int32, 0.1, 0.1),
     (140001, 5000, 8, F32, torch.int64, 0.3, 0.1),   # counts scanned by a kernel of their own
 ]
 
@@ -345,8 +348,11 @@ ROUTE = [  # tokens, k, experts, d, dtype, index, dropped
     (3000, 64, 70, 8, BF16, torch.int64, 0.05),
     (2049, 8, 256, 128, F32, torch.int64, 0),
     (5, 3, 2, 16384, BF16, torch.int32, 0.2),
-    (512, 4, 16, 24, BF16, torch.int64, 0.1),         # the most of one tile
+    (512, 4, 16, 24, BF16, torch.int64, 0.1),         # the most of one CTA
     (683, 3, 9, 24, F32, torch.int64, 0.1),           # one entry more
+    (5461, 3, 40, 8, BF16, torch.int64, 0.1),         # eight CTAs, one short
+    (8192, 2, 7, 8, BF16, torch.int64, 0.1),          # the most of a cluster
+    (3277, 5, 40, 8, BF16, torch.int64, 0.1),         # one more than it takes
     (17001, 8, 300, 8, BF16, torch.int64, 0.1),
     (70001, 2, 33, 8, F32, torch.int32, 0.1),
 ]

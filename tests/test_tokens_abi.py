@@ -146,8 +146,8 @@ def test_vectors_are_needed_and_aligned_to_their_values(L, call, shape, names):
     (sort, route, "lsh_attn_route_sort_workspace_size")])
 @pytest.mark.parametrize("dtype", [lsh.BF16, lsh.F32])
 def test_workspaces_are_sized_and_checked(L, call, shape, query, dtype):
-    # (up to 2048 entries are sorted in one block, without a workspace)
-    s, n = shape(dtype=dtype, **({"tokens": 5000} if shape is route else {})), ctypes.c_size_t()
+    # (up to 16384 entries are sorted by expert without a workspace)
+    s, n = shape(dtype=dtype, **({"tokens": 40000} if shape is route else {})), ctypes.c_size_t()
     assert getattr(L, query)(ref(s), ctypes.byref(n)) == 0
     assert n.value > 0
     assert call(L, s, n=n.value - 1) == 3
