@@ -129,7 +129,7 @@ struct KeyOrder {
   int2* runs;         // [K] the slots [x, y) of each key that occurs (needs sorted and present)
   uint32_t* present;  // [(K + 31) / 32] bit k: key k occurs
   int32_t* zeros;     // cleared for a later kernel (with runs)
-  int n_zeros;        // at most n
+  int n_zeros;
 };
 size_t key_sort_scratch_bytes(long long n, int K);
 cudaError_t launch_key_sort(long long n, int K, const void* keys, bool keys64, const KeyOrder& o,

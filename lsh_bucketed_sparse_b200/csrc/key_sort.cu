@@ -399,15 +399,13 @@ key_scatter_kernel(const S src, const int32_t* __restrict__ cnt, const int32_t* 
   place_warp<kPer>(key, entry, peers, mine, shift, mask, lane, perm, undo, sorted);
 }
 
-// Runs of the finished order; zeros[0, n_zeros) = 0 for the kernel after
-// (n_zeros <= n).
+// Runs of the finished order; zeros[0, n_zeros) = 0 for the kernel after.
 __global__ void __launch_bounds__(kThreads)
 key_runs_kernel(const KeyOrder o, int n, int K) {
   wait_prior_grid();
   const int s = blockIdx.x * kThreads + threadIdx.x;
-  if (s >= n) return;
-  if (s < o.n_zeros) o.zeros[s] = 0;
-  mark_run(o.sorted, s, n, K, o.runs, o.present);
+  for (int i = s; i < o.n_zeros; i += gridDim.x * kThreads) o.zeros[i] = 0;
+  if (s < n) mark_run(o.sorted, s, n, K, o.runs, o.present);
 }
 
 // ---------------------------------------------------------------- host side
