@@ -711,10 +711,11 @@ int pairs_of_device() { return std::max(1, sm_count() / 2); }
 
 // Clock cycles per K block of a tile of `width` columns: the pair's tensor
 // cores take 2 per column and product, but what a CTA has to fetch for it
-// (16 KB of A, half the columns of B, of each plane) comes at some 48 bytes a
-// cycle.
+// (16 KB of A, half the columns of B, of each plane) takes longer where there
+// is one product.  Fitted to tiles of 256 and 192 (K of 9472), with planes of
+// 256, 192 and 128 columns (K of 520: 3840, 3415 and 2846 cycles a block).
 double block_cycles(int width, bool planes) {
-  return planes ? std::max(2.0 * 6 * width, 3 * (341 + 1.33 * width))
+  return planes ? std::max(12.0 * width, 1520 + 7.8 * width)
                 : std::max(2.0 * width, 341 + 1.33 * width);
 }
 constexpr double kTileCycles = 3000;  // to fill and empty the pipeline
