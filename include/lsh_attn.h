@@ -369,7 +369,9 @@ LSH_ATTN_API lsh_status lsh_attn_embed_backward(const lsh_table* shape, const vo
  *   z_iv = scale x_i . table_v,  lse_i = log sum_v exp(z_iv),
  *   loss_i = lse_i - z_i,targets_i, and 0 for padding (lse is still given).
  *   x [n, D] dtype; table [V, D] dtype; targets [n] index type; loss, lse
- *   [n] float32 out.
+ *   [n] float32 out.  float32 values are taken apart for the tensor cores: an
+ *   infinite one makes the logits that it takes part in NaN (not so with
+ *   LSH_FLAG_PORTABLE).
  *   workspace: at least lsh_attn_xent_workspace_size() bytes, 256-byte
  *   aligned (may be NULL when that is 0).                                   */
 LSH_ATTN_API lsh_status lsh_attn_xent_workspace_size(const lsh_table* shape, size_t* bytes);
@@ -384,6 +386,7 @@ LSH_ATTN_API lsh_status lsh_attn_xent(const lsh_table* shape, const void* x, con
  * dtable, whatever x and dloss hold there.
  *   dx [n, D] dtype out; dtable [V, D] dtype out.  With bfloat16, g is rounded
  *   to bfloat16 before the two products; they are summed in float32.
+ *   The work is that of the rows that have a target.
  *   workspace: at least lsh_attn_xent_backward_workspace_size() bytes,
  *   256-byte aligned (may be NULL when that is 0).                          */
 LSH_ATTN_API lsh_status lsh_attn_xent_backward_workspace_size(const lsh_table* shape,
