@@ -47,6 +47,7 @@ constexpr int kStaging = 32 * 128;  // bytes per epilogue warp: 32 rows of 128 b
 constexpr int kBars = 2 * kSlots + 5;
 constexpr int kSmem = 1024 + kSlots * kSlotBytes + kEpiWarps * kStaging + kBars * 8 + 16;
 static_assert(kSmem <= 227 * 1024, "shared memory");
+constexpr float kBf16Max = 3.3895313892515355e38f;
 
 enum class Epi { kLse, kGrad, kStore, kAdd };
 
@@ -611,14 +612,21 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
 }
 
 // ---------------------------------------------------------------- preparation
-// Eight values to the three planes of piece i of `pieces`.
+// Eight values to the three planes of piece i of `pieces`.  (The first plane
+// stops at bfloat16's largest value: float32's largest would round to infinity
+// there.  The rest goes to the second.)
 __device__ __forceinline__ void put_planes(__nv_bfloat16* planes, long long pieces, long long i,
                                            float* f) {
 #pragma unroll
   for (int pl = 0; pl < 3; ++pl) {
-    Vec16<__nv_bfloat16>::store(planes + ((size_t)pl * pieces + i) * 8, f);
+    float b[8];
 #pragma unroll
-    for (int t = 0; t < 8; ++t) f[t] -= __bfloat162float(__float2bfloat16_rn(f[t]));
+    for (int t = 0; t < 8; ++t) {
+      b[t] = __bfloat162float(__float2bfloat16_rn(f[t]));
+      if (isinf(b[t]) && !isinf(f[t])) b[t] = copysignf(kBf16Max, f[t]);
+      f[t] -= b[t];
+    }
+    Vec16<__nv_bfloat16>::store(planes + ((size_t)pl * pieces + i) * 8, b);
   }
 }
 

@@ -259,6 +259,30 @@ def test_words_at_minus_infinity_take_no_part():
     R.check("loss", loss, (want, bound))
 
 
+@pytest.mark.parametrize("portable", [False, True])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_words_masked_by_the_lowest_value_take_no_part(dtype, portable):
+    # x's last column is 1, a masked word's entry there the type's lowest value
+    g = gen(13)
+    x, table = randn(g, 140, 64, dtype=dtype), randn(g, 400, 64, dtype=dtype, scale=0.1)
+    x[:, -1] = 1
+    masked = torch.rand(400, device=DEV, generator=g) < 0.3
+    table[masked, -1] = torch.finfo(dtype).min
+    keep = torch.nonzero(~masked)[:, 0]
+    at = torch.randint(0, keep.numel(), (140,), device=DEV, generator=g)
+    dloss = randn(g, 140)
+    loss, lse = lsh.lsh_attn_xent(x, table, keep[at], portable=portable)
+    want_loss, want_lse = R.xent(x, table[keep], at, 1.0)
+    R.check("lse", lse, want_lse)
+    R.check("loss", loss, want_loss)
+    dx, dw = lsh.lsh_attn_xent_backward(x, table, keep[at], lse, dloss, portable=portable)
+    want_dx, want_dw = R.xent_backward(x, table[keep], at, dloss, 1.0,
+                                       BF16 if dtype == BF16 and not portable else None)
+    R.check("dx", dx, want_dx)
+    R.check("dtable", dw[keep], want_dw)
+    assert not bool(dw[masked].any())
+
+
 def test_a_nan_in_a_row_stays_in_that_row():
     x, table, t, dloss = make_xent(200, 300, 64, BF16, torch.int64, 0)
     x[7, 3] = float("nan")
