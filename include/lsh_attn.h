@@ -2,7 +2,8 @@
  * lsh_attn.h -- C ABI of liblsh_attn.so, LSH attention for the B200 (sm_100a)
  * and, further down, the operators of a language model around it (token table
  * and cross entropy, tokens sorted by expert).  The attention is shared-QK
- * attention restricted by random-rotation hashing, as described in "Reformer: The Efficient Transformer" (arXiv 2001.04451v2):
+ * attention restricted by random-rotation hashing, as described in "Reformer:
+ * The Efficient Transformer" (arXiv 2001.04451v2):
  *   section 2 "LSH attention"     -- hash h(x) = argmax([xR; -xR]), sort by
  *                                    bucket, attend within sorted chunks;
  *   section 2 "Causal masking"    -- positions follow the same permutation,

@@ -526,6 +526,10 @@ class _launching:
             h.__exit__(*exc)
 
 
+def _at(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
 def _size(query, shape) -> int:
     n = _SZ()
     _check(query(ctypes.byref(shape), ctypes.byref(n)))
@@ -565,7 +569,7 @@ def lsh_attn_embed(tokens, table, *, scale=1.0, out=None, stream=None):
     shp = make_table_shape(tokens.numel(), V, D, table.dtype, _index_code(tokens, "tokens"), scale)
     with _launching(tokens.device, stream) as st:
         out = _out(out, "out", table.dtype, (*tokens.shape, D), tokens)
-        _check(lib().lsh_attn_embed(ctypes.byref(shp), tokens.data_ptr(), table.data_ptr(), out.data_ptr(), st))
+        _check(lib().lsh_attn_embed(ctypes.byref(shp), _at(tokens), _at(table), _at(out), st))
     return out
 
 
@@ -593,8 +597,8 @@ def lsh_attn_embed_backward(tokens, dout, vocab, *, scale=1.0, init=None, out=No
     with _launching(tokens.device, stream) as st:
         out = _out(out, "out", dout.dtype, (vocab, D), tokens)
         ws, n = _workspace(workspace, need, tokens)
-        _check(lib().lsh_attn_embed_backward(ctypes.byref(shp), tokens.data_ptr(), dout.data_ptr(),
-                                             (None if init is None else init.data_ptr()), out.data_ptr(), (None if ws is None else ws.data_ptr()), n, st))
+        _check(lib().lsh_attn_embed_backward(ctypes.byref(shp), _at(tokens), _at(dout), _at(init),
+                                             _at(out), _at(ws), n, st))
     return out
 
 
@@ -624,8 +628,8 @@ def lsh_attn_xent(x, table, targets, *, scale=1.0, workspace=None, portable=Fals
     with _launching(x.device, stream) as st:
         loss, lse = x.new_empty((2, *targets.shape), dtype=torch.float32).unbind(0)
         ws, n = _workspace(workspace, need, x)
-        _check(lib().lsh_attn_xent(ctypes.byref(shp), x.data_ptr(), table.data_ptr(), targets.data_ptr(),
-                                   loss.data_ptr(), lse.data_ptr(), (None if ws is None else ws.data_ptr()), n, st))
+        _check(lib().lsh_attn_xent(ctypes.byref(shp), _at(x), _at(table), _at(targets), _at(loss),
+                                   _at(lse), _at(ws), n, st))
     return loss, lse
 
 
@@ -644,9 +648,9 @@ def lsh_attn_xent_backward(x, table, targets, lse, dloss, *, scale=1.0, workspac
     with _launching(x.device, stream) as st:
         dx, dtable = torch.empty_like(x), torch.empty_like(table)
         ws, n = _workspace(workspace, need, x)
-        _check(lib().lsh_attn_xent_backward(ctypes.byref(shp), x.data_ptr(), table.data_ptr(),
-                                            targets.data_ptr(), lse.data_ptr(), dloss.data_ptr(), dx.data_ptr(),
-                                            dtable.data_ptr(), (None if ws is None else ws.data_ptr()), n, st))
+        _check(lib().lsh_attn_xent_backward(ctypes.byref(shp), _at(x), _at(table), _at(targets),
+                                            _at(lse), _at(dloss), _at(dx), _at(dtable), _at(ws), n,
+                                            st))
     return dx, dtable
 
 
@@ -671,8 +675,8 @@ def lsh_attn_route_sort(experts, n_experts, *, workspace=None, stream=None):
         undo = experts.new_empty((T, k), dtype=torch.int32)
         offsets = experts.new_empty(n_experts + 1, dtype=torch.int32)
         ws, n = _workspace(workspace, need, experts)
-        _check(lib().lsh_attn_route_sort(ctypes.byref(shp), experts.data_ptr(), perm.data_ptr(), undo.data_ptr(),
-                                         offsets.data_ptr(), (None if ws is None else ws.data_ptr()), n, st))
+        _check(lib().lsh_attn_route_sort(ctypes.byref(shp), _at(experts), _at(perm), _at(undo),
+                                         _at(offsets), _at(ws), n, st))
     return perm, undo, offsets
 
 
@@ -698,8 +702,8 @@ def lsh_attn_route_gather(x, undo, offsets, *, out=None, stream=None):
     shp = _route_args(x, "x", False, undo, offsets)
     with _launching(x.device, stream) as st:
         out = _out(out, "out", x.dtype, (undo.numel(), x.shape[1]), x)
-        _check(lib().lsh_attn_route_gather(ctypes.byref(shp), x.data_ptr(), undo.data_ptr(), offsets.data_ptr(),
-                                           out.data_ptr(), st))
+        _check(lib().lsh_attn_route_gather(ctypes.byref(shp), _at(x), _at(undo), _at(offsets),
+                                           _at(out), st))
     return out
 
 
@@ -709,8 +713,8 @@ def lsh_attn_route_gather_backward(dxs, undo, offsets, *, out=None, stream=None)
     shp = _route_args(dxs, "dxs", True, undo, offsets)
     with _launching(dxs.device, stream) as st:
         out = _out(out, "out", dxs.dtype, (undo.shape[0], dxs.shape[1]), dxs)
-        _check(lib().lsh_attn_route_gather_backward(ctypes.byref(shp), dxs.data_ptr(), undo.data_ptr(),
-                                                    offsets.data_ptr(), out.data_ptr(), st))
+        _check(lib().lsh_attn_route_gather_backward(ctypes.byref(shp), _at(dxs), _at(undo),
+                                                    _at(offsets), _at(out), st))
     return out
 
 
@@ -721,8 +725,8 @@ def lsh_attn_route_combine(y, weights, undo, offsets, *, out=None, stream=None):
     _cuda(weights, "weights", torch.float32, undo.shape, y)
     with _launching(y.device, stream) as st:
         out = _out(out, "out", y.dtype, (undo.shape[0], y.shape[1]), y)
-        _check(lib().lsh_attn_route_combine(ctypes.byref(shp), y.data_ptr(), weights.data_ptr(), undo.data_ptr(),
-                                            offsets.data_ptr(), out.data_ptr(), st))
+        _check(lib().lsh_attn_route_combine(ctypes.byref(shp), _at(y), _at(weights), _at(undo),
+                                            _at(offsets), _at(out), st))
     return out
 
 
@@ -735,7 +739,7 @@ def lsh_attn_route_combine_backward(dout, y, weights, undo, offsets, *, stream=N
     with _launching(y.device, stream) as st:
         dy = torch.empty_like(y)
         dw = torch.empty_like(weights)
-        _check(lib().lsh_attn_route_combine_backward(ctypes.byref(shp), dout.data_ptr(), y.data_ptr(),
-                                                     weights.data_ptr(), undo.data_ptr(), offsets.data_ptr(),
-                                                     dy.data_ptr(), dw.data_ptr(), st))
+        _check(lib().lsh_attn_route_combine_backward(ctypes.byref(shp), _at(dout), _at(y),
+                                                     _at(weights), _at(undo), _at(offsets),
+                                                     _at(dy), _at(dw), st))
     return dy, dw

@@ -124,7 +124,7 @@ cudaError_t launch_combine(const Problem& p, const void* o_rounds, const float* 
 struct KeyOrder {
   int32_t* perm;      // [n] the entry in slot s
   int32_t* undo;      // [n] its inverse
-  int32_t* offsets;   // [K + 1] each key's first slot, then the first of those outside; K < 1024 only
+  int32_t* offsets;   // [K + 1] each key's first slot, then that of the keys outside (K < 1024)
   int32_t* sorted;    // [n] the key in slot s (K: outside)
   int2* runs;         // [K] the slots [x, y) of each key that occurs (needs sorted and present)
   uint32_t* present;  // [(K + 31) / 32] bit k: key k occurs

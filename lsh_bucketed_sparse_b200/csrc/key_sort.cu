@@ -343,7 +343,8 @@ key_scatter_kernel(const S src, const int32_t* __restrict__ cnt, const int32_t* 
                    int32_t* __restrict__ perm, int32_t* __restrict__ undo,
                    int32_t* __restrict__ sorted, int32_t* __restrict__ offsets, int n, int tiles,
                    int bins, int shift, int mask) {
-  extern __shared__ int32_t off[];  // [kWarps][bins], then without kScanned first[bins], before[bins]
+  // [kWarps][bins], then without kScanned first[bins], before[bins]
+  extern __shared__ int32_t off[];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int32_t* mine = off + (size_t)warp * bins;
   for (int b = lane; b < bins; b += 32) mine[b] = 0;

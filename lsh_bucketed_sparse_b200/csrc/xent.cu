@@ -73,9 +73,11 @@ cudaError_t launch_xent_clean(const TableProblem& p, const void* x, const void* 
   uint4* dst = static_cast<uint4*>(clean);
   cudaError_t e =
       p.idx64 ? launch_dependent(xent_clean_kernel<int64_t>, grid, block, 0, st, src,
-                                 static_cast<const int64_t*>(targets), dst, pieces, per_row, p.vocab)
+                                 static_cast<const int64_t*>(targets), dst, pieces, per_row,
+                                 p.vocab)
               : launch_dependent(xent_clean_kernel<int32_t>, grid, block, 0, st, src,
-                                 static_cast<const int32_t*>(targets), dst, pieces, per_row, p.vocab);
+                                 static_cast<const int32_t*>(targets), dst, pieces, per_row,
+                                 p.vocab);
   if (e == cudaSuccess) note_launch();
   return e;
 }

@@ -145,8 +145,8 @@ xent_g_kernel(const Operand<T> x, const Operand<T> w, const I* __restrict__ targ
   }
 }
 
-// Grid (row tiles, column tiles).  out = A B^T (+ sum, a float32 matrix of earlier pieces); to `out` when it
-// is not NULL, else back to `sum`.
+// Grid (row tiles, column tiles).  out = A B^T (+ sum, a float32 matrix of
+// earlier pieces); to `out` when it is not NULL, else back to `sum`.
 template <typename TA, typename TB, typename TO>
 __global__ void __launch_bounds__(kThreads)
 xent_product_kernel(const Operand<TA> A, const Operand<TB> B, float* sum, int first, TO* out,
@@ -250,8 +250,9 @@ cudaError_t launch_xent_portable(const TableProblem& p, const void* x, const voi
                                  const void* targets, float2* part, float* zt, cudaStream_t st) {
   const int slice = slice_of(p), slices = xent_portable_slices(p);
   if (p.bf16)
-    return p.idx64 ? fwd_t<__nv_bfloat16, int64_t>(p, x, table, targets, part, zt, slice, slices, st)
-                   : fwd_t<__nv_bfloat16, int32_t>(p, x, table, targets, part, zt, slice, slices, st);
+    return p.idx64
+               ? fwd_t<__nv_bfloat16, int64_t>(p, x, table, targets, part, zt, slice, slices, st)
+               : fwd_t<__nv_bfloat16, int32_t>(p, x, table, targets, part, zt, slice, slices, st);
   return p.idx64 ? fwd_t<float, int64_t>(p, x, table, targets, part, zt, slice, slices, st)
                  : fwd_t<float, int32_t>(p, x, table, targets, part, zt, slice, slices, st);
 }
@@ -269,11 +270,9 @@ cudaError_t launch_xent_portable_backward(const TableProblem& p, const void* x, 
   float* sum = reinterpret_cast<float*>(static_cast<char*>(workspace) +
                                         align256((size_t)p.rows * piece_of(p) * sizeof(float)));
   void* clean = reinterpret_cast<char*>(sum) + align256((size_t)p.rows * p.d * sizeof(float));
-  if (p.bf16)
-    return p.idx64 ? bwd_t<__nv_bfloat16, int64_t>(p, x, table, targets, lse, dloss, dx, dtable, g, sum, clean, st)
-                   : bwd_t<__nv_bfloat16, int32_t>(p, x, table, targets, lse, dloss, dx, dtable, g, sum, clean, st);
-  return p.idx64 ? bwd_t<float, int64_t>(p, x, table, targets, lse, dloss, dx, dtable, g, sum, clean, st)
-                 : bwd_t<float, int32_t>(p, x, table, targets, lse, dloss, dx, dtable, g, sum, clean, st);
+  auto run = p.bf16 ? (p.idx64 ? bwd_t<__nv_bfloat16, int64_t> : bwd_t<__nv_bfloat16, int32_t>)
+                    : (p.idx64 ? bwd_t<float, int64_t> : bwd_t<float, int32_t>);
+  return run(p, x, table, targets, lse, dloss, dx, dtable, g, sum, clean, st);
 }
 
 }  // namespace lsh

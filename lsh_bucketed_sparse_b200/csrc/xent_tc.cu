@@ -267,9 +267,7 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
           }
         }
       }
-      if (!ok) {
-        give_up(kErrWaitProducer);
-      }
+      if (!ok) give_up(kErrWaitProducer);
       // The last loads must land before either CTA may exit (CTA 1 waits for
       // CTA 0 at the end).
       if (rank == 0) {
@@ -347,9 +345,7 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
           }
         }
       }
-      if (!ok) {
-        give_up(kErrWaitMma);
-      }
+      if (!ok) give_up(kErrWaitMma);
       if (issued) {  // every MMA finishes before tensor memory is released
         asm volatile(
             "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
@@ -407,6 +403,10 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
     };
     auto put64 = [&](int j, uint4 w) {
       *reinterpret_cast<uint4*>(mine + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) = w;
+    };
+    // (a vote, so that a wait that runs out ends for the whole warp)
+    auto wait_tile = [&](int buf, int tile) {
+      return __all_sync(0xffffffffu, mbar_wait(&t_full[buf], (tile >> 1) & 1, abort_flag));
     };
     auto release = [&](int buf) {
       tc_fence_before_sync();
@@ -535,8 +535,8 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
         }
         if constexpr (!kPlanes) {
           const int buf = tile & 1;
-          if (!mbar_wait(&t_full[buf], (tile >> 1) & 1, abort_flag)) { ok = false; break; }
-          __syncwarp();
+          ok = wait_tile(buf, tile);
+          if (!ok) break;
           tc_fence_after_sync();
           const uint32_t from = lane_addr + (uint32_t)(buf * kTileN);
           uint32_t u[2][32];
@@ -571,8 +571,8 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
           float sum[4][32];
           for (int kc = it.k0; ok && kc < it.k1; kc += g.chunk, ++tile) {
             const int buf = tile & 1;
-            if (!mbar_wait(&t_full[buf], (tile >> 1) & 1, abort_flag)) { ok = false; break; }
-            __syncwarp();
+            ok = wait_tile(buf, tile);
+            if (!ok) break;
             tc_fence_after_sync();
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -923,7 +923,8 @@ cudaError_t launch_rows(const TableProblem& p, const void* x, const int32_t* ord
   __nv_bfloat16* to = static_cast<__nv_bfloat16*>(rows);
   cudaError_t e =
       p.bf16 ? launch_dependent(xent_rows_kernel<__nv_bfloat16>, grid, block, 0, st,
-                                static_cast<const __nv_bfloat16*>(x), order, count, to, pieces, per_row)
+                                static_cast<const __nv_bfloat16*>(x), order, count, to, pieces,
+                                per_row)
              : launch_dependent(xent_rows_kernel<float>, grid, block, 0, st,
                                 static_cast<const float*>(x), order, count, to, pieces, per_row);
   if (e == cudaSuccess) note_launch();
@@ -1099,7 +1100,8 @@ cudaError_t launch_xent_tc_backward(const TableProblem& p, const void* x, const 
     }
   }
   // dx's rows to their places
-  if (f32) return launch_sum<float, float>(dx_rows, dx, slots, count, p.rows, p.d, plan.dx.splits, st);
+  if (f32)
+    return launch_sum<float, float>(dx_rows, dx, slots, count, p.rows, p.d, plan.dx.splits, st);
   if (plan.f32_dx)
     return launch_sum<float, __nv_bfloat16>(dx_rows, dx, slots, count, p.rows, p.d, plan.dx.splits,
                                             st);
