@@ -118,10 +118,12 @@ route_combine_kernel(const T* __restrict__ y, const float* __restrict__ weights,
 }
 
 // A group of `lanes` lanes (a power of two) per token, kBatch entries at a
-// time: the token's row is read once for all of them.
+// time: the token's row is read once for all of them.  Four resident blocks
+// (64 registers) rather than the three of its own choice: 102 to 94 us for
+// 32768 tokens of 1024 bf16, four entries each (HBM: 92 us).
 constexpr int kBatch = 4;
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
 route_combine_grad_kernel(const T* __restrict__ dout, const T* __restrict__ y,
                           const float* __restrict__ weights, const int32_t* __restrict__ undo,
                           const int32_t* __restrict__ kept, T* __restrict__ dy,
