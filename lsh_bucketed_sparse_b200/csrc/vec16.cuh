@@ -62,6 +62,8 @@ struct PieceBlock {
 };
 
 // Lanes that share a row of `pieces` pieces: a power of two, 32 at most.
+// (Fewer lanes where 32 leave some idle in a row's last pass cost more than
+// those: 4093 x 264 float32, 66 pieces, 21 us with 8 lanes, 11 with 32.)
 inline int lanes_of_row(int pieces) {
   int lanes = 1;
   while (lanes < 32 && lanes < pieces) lanes *= 2;

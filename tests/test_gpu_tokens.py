@@ -372,6 +372,10 @@ ROUTE = [  # tokens, k, experts, d, dtype, index, dropped
     (3000, 64, 70, 8, BF16, torch.int64, 0.05),
     (2049, 8, 256, 128, F32, torch.int64, 0),
     (5, 3, 2, 16384, BF16, torch.int32, 0.2),
+    (1000, 1, 16, 256, BF16, torch.int64, 0.1),
+    (301, 1, 4, 1032, F32, torch.int64, 0.1),
+    (1001, 2, 16, 72, BF16, torch.int32, 0.1),
+    (77, 20, 33, 520, BF16, torch.int64, 0.1),        # entries in three batches, long rows
     (512, 4, 16, 24, BF16, torch.int64, 0.1),         # the most of one CTA
     (683, 3, 9, 24, F32, torch.int64, 0.1),           # one entry more
     (5461, 3, 40, 8, BF16, torch.int64, 0.1),         # eight CTAs, one short
