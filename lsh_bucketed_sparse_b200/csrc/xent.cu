@@ -59,6 +59,7 @@ xent_clean_kernel(const uint4* __restrict__ x, const I* __restrict__ targets,
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 int slices_of(const TableProblem& p) {
+  if (xent_few_supported(p)) return xent_few_slices(p);
   return xent_tc_supported(p) ? xent_tc_slices(p) : xent_portable_slices(p);
 }
 
@@ -86,7 +87,7 @@ size_t xent_workspace_bytes(const TableProblem& p) {
   if (p.rows == 0) return 0;
   return align256((size_t)p.rows * slices_of(p) * sizeof(float2)) +
          align256((size_t)p.rows * sizeof(float)) +
-         (xent_tc_supported(p) ? xent_tc_bytes(p) : 0);
+         (!xent_few_supported(p) && xent_tc_supported(p) ? xent_tc_bytes(p) : 0);
 }
 
 cudaError_t launch_xent(const TableProblem& p, const void* x, const void* table,
@@ -98,7 +99,8 @@ cudaError_t launch_xent(const TableProblem& p, const void* x, const void* table,
   float* zt = reinterpret_cast<float*>(static_cast<char*>(workspace) +
                                        align256((size_t)p.rows * slices * sizeof(float2)));
   void* scratch = reinterpret_cast<char*>(zt) + align256((size_t)p.rows * sizeof(float));
-  cudaError_t e = xent_tc_supported(p)
+  cudaError_t e = xent_few_supported(p) ? launch_xent_few(p, x, table, targets, part, zt, st)
+                  : xent_tc_supported(p)
                       ? launch_xent_tc(p, x, table, targets, part, zt, scratch, st)
                       : launch_xent_portable(p, x, table, targets, part, zt, st);
   if (e) return e;
@@ -117,6 +119,7 @@ cudaError_t launch_xent(const TableProblem& p, const void* x, const void* table,
 
 size_t xent_backward_workspace_bytes(const TableProblem& p) {
   if (p.rows == 0) return 0;
+  if (xent_few_supported(p)) return xent_few_backward_bytes(p);
   return xent_tc_supported(p) ? xent_tc_backward_bytes(p) : xent_portable_backward_bytes(p);
 }
 
@@ -131,6 +134,8 @@ cudaError_t launch_xent_backward(const TableProblem& p, const void* x, const voi
     if (e == cudaSuccess) note_launch();
     return e;
   }
+  if (xent_few_supported(p))
+    return launch_xent_few_backward(p, x, table, targets, lse, dloss, dx, dtable, workspace, st);
   return xent_tc_supported(p) ? launch_xent_tc_backward(p, x, table, targets, lse, dloss, dx,
                                                         dtable, workspace, st)
                               : launch_xent_portable_backward(p, x, table, targets, lse, dloss,

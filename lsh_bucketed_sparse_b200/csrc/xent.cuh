@@ -49,6 +49,16 @@ cudaError_t launch_xent_tc_backward(const TableProblem& p, const void* x, const 
                                     const void* targets, const float* lse, const float* dloss,
                                     void* dx, void* dtable, void* workspace, cudaStream_t st);
 
+// ---- few float32 rows (xent_few.cu) ----------------------------------------------
+bool xent_few_supported(const TableProblem& p);
+int xent_few_slices(const TableProblem& p);
+cudaError_t launch_xent_few(const TableProblem& p, const void* x, const void* table,
+                            const void* targets, float2* part, float* zt, cudaStream_t st);
+size_t xent_few_backward_bytes(const TableProblem& p);
+cudaError_t launch_xent_few_backward(const TableProblem& p, const void* x, const void* table,
+                                     const void* targets, const float* lse, const float* dloss,
+                                     void* dx, void* dtable, void* workspace, cudaStream_t st);
+
 // ---- CUDA cores (xent_portable.cu) ---------------------------------------------
 int xent_portable_slices(const TableProblem& p);
 cudaError_t launch_xent_portable(const TableProblem& p, const void* x, const void* table,

@@ -134,6 +134,14 @@ XENT = [  # rows, vocab, d, dtype, index, scale, holes
     (3, 70, 16384, F32, torch.int32, 1.0, 0),
     (9, 1 << 20, 16, BF16, torch.int64, 1.0, 0),
     (2, 100003, 72, F32, torch.int64, 1.0, 0),
+    (4, 3001, 136, F32, torch.int64, 1.0, 0.3),
+    (5, 31, 8, F32, torch.int32, 2.0, 0),
+    (8, 2001, 1032, F32, torch.int64, 1.0, 0.3),
+    (9, 777, 520, F32, torch.int32, 1.0, 0.2),
+    (16, 5003, 264, F32, torch.int64, -1.0, 0.1),
+    (17, 300, 128, F32, torch.int64, 1.0, 1.0),
+    (32, 1111, 1600, F32, torch.int64, 1.0, 0.2),
+    (33, 1111, 264, F32, torch.int64, 1.0, 0.2),
 ]
 
 
@@ -226,6 +234,21 @@ def test_padding_rows_may_hold_anything(dtype, portable):
     assert not bool(dx[pad].any())
     want_dx, want_dw = R.xent_backward(x, table, t, dloss, 1.0,
                                        BF16 if dtype == BF16 and not portable else None)
+    R.check("dx", dx[~pad], (want_dx[0][~pad], want_dx[1][~pad]))
+    R.check("dtable", dw, want_dw)
+
+
+@pytest.mark.parametrize("n", [3, 20])
+def test_few_rows_of_padding_may_hold_anything(n):
+    x, table, t, dloss = make_xent(n, 500, 72, F32, torch.int64, 0)
+    t[1::2] = -1
+    pad = t < 0
+    bad, up = x.clone(), dloss.clone()
+    bad[pad], up[pad] = float("nan"), float("inf")
+    loss, lse = lsh.lsh_attn_xent(bad, table, t)
+    dx, dw = lsh.lsh_attn_xent_backward(bad, table, t, lse, up)
+    assert not bool(loss[pad].any()) and not bool(dx[pad].any())
+    want_dx, want_dw = R.xent_backward(x, table, t, dloss, 1.0)
     R.check("dx", dx[~pad], (want_dx[0][~pad], want_dx[1][~pad]))
     R.check("dtable", dw, want_dw)
 
