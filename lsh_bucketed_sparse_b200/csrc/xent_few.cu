@@ -2,7 +2,7 @@
 // has the formulas).  The table is what such a call moves: it is read as it
 // stands, once for the logits, once more for both gradients, where the tensor
 // cores would need its three planes written first (one row against 131072
-// words of 1024: 112 us forward and 298 backward, 470 and 1040 through planes).
+// words of 1024: 114 us forward and 284 backward, 470 and 1040 through planes).
 // Rows are padded to kRows, a power of two.
 //
 // Logits: a warp takes R words at a time, its lanes share their columns, the
@@ -20,11 +20,14 @@
 namespace lsh {
 namespace {
 
-constexpr int kLogitThreads = 512, kLogitWarps = kLogitThreads / 32;
 constexpr size_t kMaxX = 200 * 1024;  // bytes of x in shared memory
 
-// Words per warp: as many as give 64 sums per lane, 8 at most.
-constexpr __host__ __device__ int words_of(int rows) { return rows >= 8 ? 64 / rows : 8; }
+// Words per warp.  Each float4 of a row of x, read from shared memory, serves
+// them all: with 32 rows two words (64 sums per lane) are bound by those reads,
+// four (128 sums, half the warps) by the arithmetic: 325 and 279 us for 131072
+// words of 1024.
+constexpr __host__ __device__ int words_of(int rows) { return rows >= 16 ? 4 : 8; }
+constexpr __host__ __device__ int logit_threads(int rows) { return rows >= 32 ? 256 : 512; }
 
 struct Rows {
   const float* x;
@@ -40,7 +43,8 @@ struct Rows {
 };
 
 template <int kRows, bool kGrad, typename I>
-__global__ void __launch_bounds__(kLogitThreads, 1) xent_few_logits_kernel(const Rows p) {
+__global__ void __launch_bounds__(logit_threads(kRows), 1) xent_few_logits_kernel(const Rows p) {
+  constexpr int kLogitThreads = logit_threads(kRows), kLogitWarps = kLogitThreads / 32;
   constexpr int R = words_of(kRows), kSums = kRows * R, kMine = kSums / 32;
   extern __shared__ float x_smem[];  // [kRows][d]
   __shared__ float2 joined[kLogitWarps][kRows];
@@ -153,7 +157,7 @@ __global__ void __launch_bounds__(kGradThreads)
 xent_few_grad_kernel(const Rows p, float* __restrict__ dx, float* __restrict__ dtable, int words) {
   constexpr int C = columns_of(kRows);
   using Vec = typename std::conditional<C == 2, float2, float4>::type;
-  __shared__ float g[kGradWords][kRows];
+  __shared__ __align__(16) float g[kGradWords][kRows];
   wait_prior_grid();
   const int col = (blockIdx.y * kGradThreads + threadIdx.x) * C, d = p.d;
   const bool live = col < d;
@@ -178,36 +182,55 @@ xent_few_grad_kernel(const Rows p, float* __restrict__ dx, float* __restrict__ d
   for (int i = 0; i < kRows; ++i)
     if (live && i < p.n && target_of(targets, i, p.vocab) >= 0) load(p.x + (size_t)i * d + col, x[i]);
   const int v0 = blockIdx.x * words, v1 = min(p.vocab, v0 + words);
-  for (int v = v0; v < v1; v += kGradWords) {
-    const int n = min(kGradWords, v1 - v);
-    __syncthreads();
-    for (int i = threadIdx.x; i < n * kRows; i += kGradThreads)
-      g[0][i] = p.g[(size_t)v * kRows + i];
-    __syncthreads();
-    if (!live) continue;
-    constexpr int kAhead = 4;  // words under way
-    for (int k0 = 0; k0 < n; k0 += kAhead) {
-      float w[kAhead][C];
+  // The next words and the next tile of g are under way while these are used.
+  constexpr int kAhead = 4, kMine = kGradWords * kRows / kGradThreads;
+  float w[kAhead][C], next[kAhead][C], mine[kMine];
+  auto load_words = [&](int v, float (&to)[kAhead][C]) {
 #pragma unroll
-      for (int k = 0; k < kAhead; ++k)
-        if (k0 + k < n) load(p.table + (size_t)(v + k0 + k) * d + col, w[k]);
+    for (int k = 0; k < kAhead; ++k)
+      if (live && v + k < v1) load(p.table + (size_t)(v + k) * d + col, to[k]);
+  };
+  auto load_g = [&](int v) {
+#pragma unroll
+    for (int j = 0; j < kMine; ++j) {
+      const int i = threadIdx.x + j * kGradThreads;
+      mine[j] = v + i / kRows < v1 ? p.g[(size_t)v * kRows + i] : 0.f;
+    }
+  };
+  load_g(v0);
+  load_words(v0, w);
+  for (int v = v0; v < v1; v += kGradWords) {
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < kMine; ++j) g[0][threadIdx.x + j * kGradThreads] = mine[j];
+    __syncthreads();
+    load_g(v + kGradWords);
+    for (int k0 = 0; k0 < kGradWords; k0 += kAhead) {
+      load_words(v + k0 + kAhead, next);
 #pragma unroll
       for (int k = 0; k < kAhead; ++k) {
-        if (k0 + k >= n) continue;
+        if (!live || v + k0 + k >= v1) continue;
         float dw[C];
 #pragma unroll
         for (int t = 0; t < C; ++t) dw[t] = 0.f;
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-          const float gi = g[k0 + k][i];
+        for (int i = 0; i < kRows; i += 4) {
+          const float4 g4 = *reinterpret_cast<const float4*>(&g[k0 + k][i]);
+          const float gi[4] = {g4.x, g4.y, g4.z, g4.w};
 #pragma unroll
-          for (int t = 0; t < C; ++t) {
-            a[i][t] = fmaf(gi, w[k][t], a[i][t]);
-            dw[t] = fmaf(gi, x[i][t], dw[t]);
-          }
+          for (int j = 0; j < 4; ++j)
+#pragma unroll
+            for (int t = 0; t < C; ++t) {
+              a[i + j][t] = fmaf(gi[j], w[k][t], a[i + j][t]);
+              dw[t] = fmaf(gi[j], x[i + j][t], dw[t]);
+            }
         }
         store(dtable + (size_t)(v + k0 + k) * d + col, dw);
       }
+#pragma unroll
+      for (int k = 0; k < kAhead; ++k)
+#pragma unroll
+        for (int t = 0; t < C; ++t) w[k][t] = next[k][t];
     }
   }
   if (!live) return;
@@ -253,7 +276,7 @@ int padded_rows(const TableProblem& p) {
 }
 
 int logit_blocks(const TableProblem& p) {
-  const int words = kLogitWarps * words_of(padded_rows(p));
+  const int words = logit_threads(padded_rows(p)) / 32 * words_of(padded_rows(p));
   const int all = (p.vocab + words - 1) / words;
   return all < sm_count() ? all : sm_count();
 }
@@ -276,7 +299,7 @@ cudaError_t logits_t(const TableProblem& p, const Rows& r, cudaStream_t st) {
   if (smem > 40 * 1024 &&
       (e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem)))
     return e;
-  e = launch_dependent(kernel, dim3(logit_blocks(p)), dim3(kLogitThreads), smem, st, r);
+  e = launch_dependent(kernel, dim3(logit_blocks(p)), dim3(logit_threads(kRows)), smem, st, r);
   if (e == cudaSuccess) note_launch();
   return e;
 }
