@@ -329,6 +329,8 @@ LSH_ATTN_API lsh_status lsh_attn_forward_noalloc(const lsh_shape* shape, const v
  *   flags     0 or LSH_FLAG_PORTABLE (cross entropy: CUDA cores only).
  * A token or target outside [0, V) is no error: padding (-1, say) gives a row
  * of zeros, no loss and no gradient.
+ * Workspace sizes are for the current device; a workspace serves one call at
+ * a time.
  * ---------------------------------------------------------------------- */
 typedef enum lsh_index_type {
   LSH_I32 = 0,                 /* int32 */

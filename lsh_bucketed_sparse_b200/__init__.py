@@ -511,15 +511,14 @@ class _launching:
         self.device, self.stream, self.held = device, stream, ()
 
     def __enter__(self):
+        index = self.device.index
         if self.stream is not None:
             self.held = (torch.cuda.device(self.device), torch.cuda.stream(self.stream))
-        elif torch._C._cuda_getDevice() != self.device.index:
+        elif torch._C._cuda_getDevice() != index:
             self.held = (torch.cuda.device(self.device),)
         for h in self.held:
             h.__enter__()
-        if self.stream is not None:
-            return self.stream.cuda_stream
-        return torch._C._cuda_getCurrentRawStream(self.device.index)
+        return torch._C._cuda_getCurrentRawStream(index)
 
     def __exit__(self, *exc):
         for h in reversed(self.held):
@@ -593,8 +592,8 @@ def lsh_attn_embed_backward(tokens, dout, vocab, *, scale=1.0, init=None, out=No
         _cuda(init, "init", dout.dtype, (vocab, D), tokens)
     shp = make_table_shape(tokens.numel(), vocab, D, dout.dtype, _index_code(tokens, "tokens"),
                            scale)
-    need = lsh_attn_embed_backward_workspace_size(shp)
     with _launching(tokens.device, stream) as st:
+        need = lsh_attn_embed_backward_workspace_size(shp)
         out = _out(out, "out", dout.dtype, (vocab, D), tokens)
         ws, n = _workspace(workspace, need, tokens)
         _check(lib().lsh_attn_embed_backward(ctypes.byref(shp), _at(tokens), _at(dout), _at(init),
@@ -624,8 +623,8 @@ def lsh_attn_xent(x, table, targets, *, scale=1.0, workspace=None, portable=Fals
     [V, D], the logits scale * x @ table.T never stored.  Returns (loss, lse),
     float32 [...]; loss is 0 where the target is outside the table."""
     shp = _xent_args(x, table, targets, scale, portable)
-    need = lsh_attn_xent_workspace_size(shp)
     with _launching(x.device, stream) as st:
+        need = lsh_attn_xent_workspace_size(shp)
         loss, lse = x.new_empty((2, *targets.shape), dtype=torch.float32).unbind(0)
         ws, n = _workspace(workspace, need, x)
         _check(lib().lsh_attn_xent(ctypes.byref(shp), _at(x), _at(table), _at(targets), _at(loss),
@@ -644,8 +643,8 @@ def lsh_attn_xent_backward(x, table, targets, lse, dloss, *, scale=1.0, workspac
     shp = _xent_args(x, table, targets, scale, portable)
     _cuda(lse, "lse", torch.float32, targets.shape, x)
     _cuda(dloss, "dloss", torch.float32, targets.shape, x)
-    need = lsh_attn_xent_backward_workspace_size(shp)
     with _launching(x.device, stream) as st:
+        need = lsh_attn_xent_backward_workspace_size(shp)
         dx, dtable = torch.empty_like(x), torch.empty_like(table)
         ws, n = _workspace(workspace, need, x)
         _check(lib().lsh_attn_xent_backward(ctypes.byref(shp), _at(x), _at(table), _at(targets),
@@ -669,8 +668,8 @@ def lsh_attn_route_sort(experts, n_experts, *, workspace=None, stream=None):
         raise ValueError(f"experts must be [tokens, top_k], got shape {tuple(experts.shape)}")
     T, k = experts.shape
     shp = make_route_shape(T, k, n_experts, index_type=_index_code(experts, "experts"))
-    need = lsh_attn_route_sort_workspace_size(shp)
     with _launching(experts.device, stream) as st:
+        need = lsh_attn_route_sort_workspace_size(shp)
         perm = experts.new_empty(T * k, dtype=torch.int32)
         undo = experts.new_empty((T, k), dtype=torch.int32)
         offsets = experts.new_empty(n_experts + 1, dtype=torch.int32)
