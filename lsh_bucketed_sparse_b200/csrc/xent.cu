@@ -23,7 +23,7 @@ xent_join_kernel(const float2* __restrict__ part, const float* __restrict__ zt,
   const int row = blockIdx.x * 32 + lane;
   float m = -INFINITY, s = 0.f;
   if (row < rows) {
-#pragma unroll 4
+#pragma unroll 8
     for (int k = warp; k < slices; k += kJoinWarps) {
       const float2 p = part[(size_t)k * rows + row];
       lse_add(m, s, p.x, p.y);

@@ -697,6 +697,7 @@ xent_sum_kernel(const TS* __restrict__ sums, T* __restrict__ out,
   const long long slot = slots ? slots[row] : row;
   if (!slots || slot < *count) {
     const long long from = slot * per_row + piece;
+#pragma unroll 4
     for (int s = 0; s < planes; ++s) {
       float f[8];
       load8(sums + ((size_t)s * pieces + from) * 8, f);
@@ -741,8 +742,10 @@ void set_chunk(Gemm* g) { g->chunk = g->planes ? kPlaneChunk : g->kb_split; }
 // may_split) so that the estimated time is least: fewer columns or a part of K
 // per tile where whole tiles would leave pairs idle.  A part of K costs
 // another plane of partial sums, written and read back at HBM's rate (some
-// 4000 bytes per cycle).
+// 4000 bytes per cycle) one after another.
 void set_tiles(Gemm* g, bool may_split) {
+  static constexpr int kParts[] = {1, 2, 3, 4, 5, 6, 7, 8, 12, 16, 24, 32, 48, 64};
+  constexpr double kPlaneCycles = 200;
   const int pairs = pairs_of_device();
   double best = -1;
   for (int width = kTileN; width >= 64; width -= 64) {
@@ -750,12 +753,13 @@ void set_tiles(Gemm* g, bool may_split) {
     const int last_width = ceil_div(last, 32) * 32;  // N of a pair's MMA
     const double block = (block_cycles(width, g->planes) * (n - 1) +
                           block_cycles(last_width, g->planes)) / n;
-    for (int s = 1; s <= (may_split ? 8 : 1) && s <= g->kb; ++s) {
-      const int kb = ceil_div(g->kb, s);
-      if (ceil_div(g->kb, kb) != s) continue;
+    for (int parts : kParts) {
+      if (parts > 1 && (!may_split || parts > g->kb)) break;
+      const int kb = ceil_div(g->kb, parts), s = ceil_div(g->kb, kb);
       const double waves = ceil_div((long long)g->m_tiles * n * s, pairs);
-      const double cost = waves * (kb * block + kTileCycles) +
-                          (s > 1 ? 2.0 * s * g->rows * g->cols * 4 / 4000 : 0.0);
+      const double cost =
+          waves * (kb * block + kTileCycles) +
+          (s > 1 ? s * (kPlaneCycles + 2.0 * g->rows * g->cols * 4 / 4000) : 0.0);
       if (best >= 0 && cost >= best) continue;
       best = cost;
       g->width = width;
