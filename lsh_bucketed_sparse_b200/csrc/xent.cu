@@ -9,14 +9,17 @@ namespace {
 
 constexpr int kThreads = 256;
 
-// lse_i = log sum over the slices, loss_i = lse_i - z_i,t_i.  A block joins 32
-// rows: each warp every kJoinWarps-th slice, then the warps in order.
+// lse_i = log(R_i + exp z_i,t_i), loss_i = lse_i - z_i,t_i = log1p(R_i / exp
+// z_i,t_i), where R_i = s 2^m is the slices' sum, which leaves the target out: the
+// loss of a row that is sure of its target keeps its digits, where 1 + R_i and
+// the difference of two logits would cut them off.  A block joins 32 rows: each
+// warp every kJoinWarps-th slice, then the warps in order.
 constexpr int kJoinWarps = kThreads / 32;
 template <typename I>
 __global__ void __launch_bounds__(kThreads)
 xent_join_kernel(const float2* __restrict__ part, const float* __restrict__ zt,
                  const I* __restrict__ targets, float* __restrict__ loss, float* __restrict__ lse,
-                 int rows, int slices, int vocab) {
+                 int rows, int slices, int vocab, float unit) {
   __shared__ float2 sums[kJoinWarps][32];
   wait_prior_grid();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -34,10 +37,21 @@ xent_join_kernel(const float2* __restrict__ part, const float* __restrict__ zt,
   if (warp != 0 || row >= rows) return;
 #pragma unroll
   for (int w = 1; w < kJoinWarps; ++w) lse_add(m, s, sums[w][lane].x, sums[w][lane].y);
-  const float log_s = log2f(s);
-  lse[row] = (m + log_s) * kLn2;
-  // the target's logit next to the maximum first: they may be the same
-  loss[row] = target_of(targets, row, vocab) >= 0 ? ((m - zt[row]) + log_s) * kLn2 : 0.f;
+  if (target_of(targets, row, vocab) < 0) {
+    lse[row] = (m + log2f(s)) * kLn2;
+    loss[row] = 0.f;
+    return;
+  }
+  const float z = zt[row], d = fmaf(-z, unit, m);  // m against the target, in one rounding
+  if (unit == 0.f) {  // all logits are 0, the target's among s
+    lse[row] = loss[row] = (d + log2f(s)) * kLn2;
+    return;
+  }
+  const float over = d > 0.f ? (d + log2f(s + exp2f(-d))) * kLn2 : log1pf(s * exp2f(d));
+  lse_add(m, s, z * unit, 1.f);
+  const float all = (m + log2f(s)) * kLn2;
+  lse[row] = all;
+  loss[row] = isnan(all) ? all : over;
 }
 
 __global__ void __launch_bounds__(kThreads) xent_zero_kernel(uint4* out, long long pieces) {
@@ -105,14 +119,16 @@ cudaError_t launch_xent(const TableProblem& p, const void* x, const void* table,
                       : launch_xent_portable(p, x, table, targets, part, zt, st);
   if (e) return e;
   const dim3 grid((rows + 31) / 32), block(kThreads);
+  const float unit =
+      !xent_few_supported(p) && xent_tc_supported(p) ? p.scale * kLog2e : 1.f;  // of zt
   e = p.idx64 ? launch_dependent(xent_join_kernel<int64_t>, grid, block, 0, st,
                                  static_cast<const float2*>(part), static_cast<const float*>(zt),
                                  static_cast<const int64_t*>(targets), loss, lse, rows, slices,
-                                 p.vocab)
+                                 p.vocab, unit)
               : launch_dependent(xent_join_kernel<int32_t>, grid, block, 0, st,
                                  static_cast<const float2*>(part), static_cast<const float*>(zt),
                                  static_cast<const int32_t*>(targets), loss, lse, rows, slices,
-                                 p.vocab);
+                                 p.vocab, unit);
   if (e == cudaSuccess) note_launch();
   return e;
 }

@@ -31,8 +31,10 @@ __device__ __forceinline__ void lse_add(float& m, float& s, float m2, float s2) 
 cudaError_t launch_xent_clean(const TableProblem& p, const void* x, const void* targets,
                               void* clean, cudaStream_t st);
 
-// Forward, of either kind: part[slice][row] = (maximum, sum) over the slice's
-// logits, zt[row] the target's logit where the row has a target, in log2.
+// Forward, of any kind: part[slice][row] = (maximum, sum) over the slice's logits
+// except the target's, which stands in zt[row] where the row has a target: in
+// log2, or from the tensor cores as the product left it, without scale (where
+// scale is 0 the sum has it too).
 
 // ---- tensor cores (xent_tc.cu) ---------------------------------------------------
 bool xent_tc_supported(const TableProblem& p);

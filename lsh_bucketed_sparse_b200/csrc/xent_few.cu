@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(logit_threads(kRows), 1) xent_few_logits_kerne
       } else {
         const float z = a[t] * c;
         if (word == target) p.zt[row] = z;
-        lse_add(run_m, run_s, z, 1.f);
+        else lse_add(run_m, run_s, z, 1.f);
       }
     }
   }

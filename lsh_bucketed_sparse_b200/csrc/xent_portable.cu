@@ -99,7 +99,7 @@ xent_fwd_kernel(const Operand<T> x, const Operand<T> w, const I* __restrict__ ta
         if (v >= v1) continue;
         const float z = acc[i][j] * scale2;
         if (v == t[i]) zt[m0 + 4 * ty + i] = z;
-        lse_add(m[i], sum[i], z, 1.f);
+        else lse_add(m[i], sum[i], z, 1.f);
       }
   }
 #pragma unroll

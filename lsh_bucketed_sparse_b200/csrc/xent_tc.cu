@@ -57,6 +57,7 @@ struct Gemm {
   int run, slices;        // n tiles of one work item, items per m tile
   int splits, kb_split;   // K in `splits` parts of kb_split blocks
   int kb;                 // K blocks of 64
+  int a_planes;           // bf16 A: one plane or two, block by block of K
   bool planes;            // float32 operands
   int chunk;              // K blocks summed in one accumulator
   int group;              // m tiles that are walked together
@@ -99,7 +100,7 @@ __device__ __forceinline__ Item decode(const Gemm& g, int item) {
   it.n0 = q / size * g.run;
   it.n1 = min(g.n_tiles, it.n0 + g.run);
   it.k0 = it.split * g.kb_split;
-  it.k1 = min(g.kb, it.k0 + g.kb_split);
+  it.k1 = min(g.kb * g.a_planes, it.k0 + g.kb_split);
   return it;
 }
 
@@ -162,8 +163,9 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 
-// T: type of D in memory; kPlanes: float32 operands in three planes each.
-template <Epi kEpi, typename T, typename I, bool kPlanes>
+// T: type of D in memory; kPlanes: float32 operands in three planes each;
+// kFine: bfloat16 operands of few rows (kFineRows below).
+template <Epi kEpi, typename T, typename I, bool kPlanes, bool kFine = false>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
                const __grid_constant__ CUtensorMap omap, const Params p) {
@@ -213,7 +215,7 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
     const int count = *p.count;
     if (p.count_k) {
       g.kb = (count + kBlockK - 1) / kBlockK;
-      g.kb_split = (g.kb + g.splits - 1) / g.splits;
+      g.kb_split = (g.kb * g.a_planes + g.splits - 1) / g.splits;
     } else {
       g.rows = count;
       g.m_tiles = (count + kTileM - 1) / kTileM;
@@ -238,7 +240,9 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
           const int nw = n == g.n_tiles - 1 ? g.last_width : g.width;
           const int c0 = n * g.width + rank * (nw / 2);
           for (int kb = it.k0; ok && kb < it.k1; ++kb, ++n_loads) {
-            const int k = kb * kBlockK;
+            // two planes of A meet the same block of B one after the other
+            const int first = !kPlanes && g.a_planes == 2 ? kb & 1 : 0;
+            const int k = (!kPlanes && g.a_planes == 2 ? kb >> 1 : kb) * kBlockK;
             // planes in the order in which their slots become free
 #pragma unroll
             for (int z = kOps - 1; z >= 0; --z) {
@@ -252,10 +256,10 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
               uint8_t* a = smem + s * kSlotBytes;
               uint8_t* b = a + kOperand;
               if (g.a_mn) {
-                tma_load_3d_pair(a, &amap, bar, m0, k, z);
-                tma_load_3d_pair(a + 8192, &amap, bar, m0 + 64, k, z);
+                tma_load_3d_pair(a, &amap, bar, m0, k, first + z);
+                tma_load_3d_pair(a + 8192, &amap, bar, m0 + 64, k, first + z);
               } else {
-                tma_load_3d_pair(a, &amap, bar, k, m0, z);
+                tma_load_3d_pair(a, &amap, bar, k, m0, first + z);
               }
               if (g.b_mn) {
                 for (int j = 0; j < b_boxes; ++j)
@@ -372,12 +376,13 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
     };
     // g is written up to the end of the K block that holds its last row
     const int row_end = kEpi == Epi::kGrad ? (g.rows + kBlockK - 1) / kBlockK * kBlockK : g.rows;
-    auto send = [&](int x, int y, int plane) {
+    auto send = [&](int x, int y, int plane, int planes = 1) {  // from `mine`, 2 KB each
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0 && x < g.cols && y < row_end && y < p.g.rows) {
         if constexpr (kEpi == Epi::kAdd) tma_add_3d(&omap, mine, x, y, plane);
-        else tma_store_3d(&omap, mine, x, y, plane);
+        else
+          for (int i = 0; i < planes; ++i) tma_store_3d(&omap, mine + i * 2048, x, y, plane + i);
         bulk_commit();
       }
     };
@@ -401,8 +406,8 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
     auto put128 = [&](int j, uint4 w) {
       *reinterpret_cast<uint4*>(mine + lane * 128 + ((j ^ (lane & 7)) << 4)) = w;
     };
-    auto put64 = [&](int j, uint4 w) {
-      *reinterpret_cast<uint4*>(mine + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) = w;
+    auto put64 = [&](int j, uint4 w, int plane = 0) {
+      *reinterpret_cast<uint4*>(mine + plane * 2048 + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) = w;
     };
     // (a vote, so that a wait that runs out ends for the whole warp)
     auto wait_tile = [&](int buf, int tile) {
@@ -439,7 +444,10 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
           if ((unsigned)(target - cc) < 32u) {
 #pragma unroll
             for (int i = 0; i < 32; ++i)
-              if (target - cc == i) p.zt[row] = z[i] * c;
+              if (target - cc == i) {
+                p.zt[row] = z[i];
+                if (c != 0.f) z[i] = c > 0.f ? -INFINITY : INFINITY;  // 2^(z c) = 0
+              }
           }
           if (there >= 32) {
             const float top = fmaxf(run_m, (c >= 0.f ? extreme<true>(z) : extreme<false>(z)) * c);
@@ -490,7 +498,12 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
 #pragma unroll
             for (int i = 0; i < 32; ++i) z[i] = 0.f;
           }
-          if constexpr (kPlanes) {
+          if constexpr (kFine) {
+            stage_free();
+#pragma unroll
+            for (int j = 0; j < 8; ++j) put64(j & 3, pack8(z + 8 * (j & 3), j < 4), j >> 2);
+            send(cc, row0, 0, 2);
+          } else if constexpr (kPlanes) {
 #pragma unroll
             for (int pl = 0; pl < 3; ++pl) {
               stage_free();
@@ -533,7 +546,7 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
           }
           continue;
         }
-        if constexpr (!kPlanes) {
+        if constexpr (!kPlanes && !kFine) {
           const int buf = tile & 1;
           ok = wait_tile(buf, tile);
           if (!ok) break;
@@ -738,6 +751,19 @@ constexpr double kTileCycles = 3000;  // to fill and empty the pipeline
 constexpr int kPlaneChunk = 2;
 void set_chunk(Gemm* g) { g->chunk = g->planes ? kPlaneChunk : g->kb_split; }
 
+// Up to so many bfloat16 rows, where the products wait for the table and half
+// of a tile's 256 rows is empty, two things are done that more rows could not
+// pay for.  The logits' accumulators are cut every kFineChunk blocks, too (a loss
+// of one row off by 4e-6 of its logits' 15 otherwise, now 7e-7).  And g has two
+// bfloat16 planes, 16 bits of significand, which keeps its rounding out of dx and
+// dW (off by 0.0017, their own rounding; with one plane by 0.0025 to 0.004): the
+// second plane is more rows of the same tile for dx, more of a short K for dW.
+// 131072 words of 1024: 16 rows 82 us forward and 223 backward (without: 76 and
+// 188), 128 rows 82 and 264 (74 and 197); 256 rows would go from 227 to 365.
+constexpr int kFineRows = 128, kFineChunk = 4;
+bool is_fine(const TableProblem& p) { return p.bf16 && p.rows <= kFineRows; }
+int g_planes_of(const TableProblem& p) { return !p.bf16 ? 3 : is_fine(p) ? 2 : 1; }
+
 // Cuts D's columns into tiles (of a multiple of 64) and K into parts (with
 // may_split) so that the estimated time is least: fewer columns or a part of K
 // per tile where whole tiles would leave pairs idle.  A part of K costs
@@ -753,9 +779,10 @@ void set_tiles(Gemm* g, bool may_split) {
     const int last_width = ceil_div(last, 32) * 32;  // N of a pair's MMA
     const double block = (block_cycles(width, g->planes) * (n - 1) +
                           block_cycles(last_width, g->planes)) / n;
+    const int blocks = g->kb * g->a_planes;
     for (int parts : kParts) {
-      if (parts > 1 && (!may_split || parts > g->kb)) break;
-      const int kb = ceil_div(g->kb, parts), s = ceil_div(g->kb, kb);
+      if (parts > 1 && (!may_split || parts > blocks)) break;
+      const int kb = ceil_div(blocks, parts), s = ceil_div(blocks, kb);
       const double waves = ceil_div((long long)g->m_tiles * n * s, pairs);
       const double cost =
           waves * (kb * block + kTileCycles) +
@@ -775,8 +802,10 @@ void set_tiles(Gemm* g, bool may_split) {
   set_chunk(g);
 }
 
-Gemm make_gemm(long long rows, int cols, int k, bool f32, bool a_mn, bool b_mn, bool may_split) {
+Gemm make_gemm(long long rows, int cols, int k, bool f32, bool a_mn, bool b_mn, bool may_split,
+               int a_planes = 1) {
   Gemm g = {};
+  g.a_planes = a_planes;
   g.rows = (int)rows;
   g.cols = cols;
   g.m_tiles = ceil_div(rows, kTileM);
@@ -806,6 +835,7 @@ Gemm logits_gemm(const TableProblem& p) {
   g.slices = ceil_div(g.n_tiles, g.run);
   g.items = g.m_tiles * g.slices;
   g.group = 64;
+  if (is_fine(p)) g.chunk = kFineChunk;
   return g;
 }
 
@@ -817,15 +847,17 @@ struct Backward {
   int words, pieces;
   size_t ld;             // columns of g
   bool f32_dx, sum_dw;   // dx's rows in float32; dW's sums outside the result
+  int dx_planes;         // sums of dx's rows
   Gemm dx, dw;           // of a whole piece
   size_t order, slots, count, rows, w_planes, g, dx_rows, dw_sums, sort, total;
 };
 
 Backward plan_backward(const TableProblem& p) {
   Backward b;
-  const int planes = p.bf16 ? 1 : 3, pairs = pairs_of_device();
+  const int planes = p.bf16 ? 1 : 3, g_planes = g_planes_of(p), pairs = pairs_of_device();
+  const bool fine = is_fine(p);
   const int all = ceil_div(p.vocab, kTileM), nt = ceil_div(p.d, kTileN);
-  const size_t per_tile = (size_t)planes * p.rows * kTileM * 2;
+  const size_t per_tile = (size_t)g_planes * p.rows * kTileM * 2;
   const int most = (int)std::min<size_t>(all, std::max<size_t>(1, kGradBytes / per_tile));
   int tiles = most;
   if (most < all) {
@@ -841,9 +873,11 @@ Backward plan_backward(const TableProblem& p) {
   b.pieces = ceil_div(all, tiles);
   b.ld = (size_t)b.words;
   const int words = std::min(b.words, p.vocab);
-  b.dx = make_gemm(p.rows, p.d, words, !p.bf16, false, true, true);
-  b.dw = make_gemm(words, p.d, (int)p.rows, !p.bf16, true, true, true);
-  b.f32_dx = !p.bf16 || b.dx.splits > 1 || b.pieces > 1;
+  // (two planes of g are twice the rows for dx, in the same tile, and twice K for dW)
+  b.dx = make_gemm(p.rows * (fine ? 2 : 1), p.d, words, !p.bf16, false, true, true);
+  b.dw = make_gemm(words, p.d, (int)p.rows, !p.bf16, true, true, true, fine ? 2 : 1);
+  b.dx_planes = b.dx.splits * (fine ? 2 : 1);
+  b.f32_dx = !p.bf16 || fine || b.dx.splits > 1 || b.pieces > 1;
   b.sum_dw = b.dw.splits > 1;
   const size_t n = (size_t)p.rows, nd = n * p.d, vd = (size_t)b.words * p.d;
   size_t off = 0;
@@ -852,8 +886,8 @@ Backward plan_backward(const TableProblem& p) {
   b.count = off;    off += 256;
   b.rows = off;     off += align256(nd * 2 * planes);
   b.w_planes = off; off += p.bf16 ? 0 : align256((size_t)p.vocab * p.d * 6);
-  b.g = off;        off += align256((size_t)planes * n * b.ld * 2);
-  b.dx_rows = off;  off += align256(nd * (b.f32_dx ? 4 : 2) * b.dx.splits);
+  b.g = off;        off += align256((size_t)g_planes * n * b.ld * 2);
+  b.dx_rows = off;  off += align256(nd * (b.f32_dx ? 4 : 2) * b.dx_planes);
   b.dw_sums = off;  off += b.sum_dw ? align256(vd * 4 * b.dw.splits) : 0;
   b.sort = off;     off += key_sort_scratch_bytes(p.rows, 1);
   b.total = off;
@@ -877,10 +911,10 @@ bool encode(CUtensorMap* map, const void* base, bool f32, long long cols, long l
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <Epi kEpi, typename T, typename I, bool kPlanes>
+template <Epi kEpi, typename T, typename I, bool kPlanes, bool kFine = false>
 cudaError_t launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o,
                    const Params& p, cudaStream_t st) {
-  auto kernel = xent_tc_kernel<kEpi, T, I, kPlanes>;
+  auto kernel = xent_tc_kernel<kEpi, T, I, kPlanes, kFine>;
   static std::atomic<unsigned long long> set{0};  // devices that know the size already
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -901,8 +935,11 @@ cudaError_t launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap
 
 // Logits or gradient of rows whose targets are int64 or int32.
 template <Epi kEpi>
-cudaError_t launch_logits(bool idx64, const CUtensorMap& a, const CUtensorMap& b,
+cudaError_t launch_logits(bool idx64, bool fine, const CUtensorMap& a, const CUtensorMap& b,
                           const CUtensorMap& o, const Params& p, cudaStream_t st) {
+  if (fine)
+    return idx64 ? launch<kEpi, __nv_bfloat16, int64_t, false, true>(a, b, o, p, st)
+                 : launch<kEpi, __nv_bfloat16, int32_t, false, true>(a, b, o, p, st);
   if (!p.g.planes)
     return idx64 ? launch<kEpi, __nv_bfloat16, int64_t, false>(a, b, o, p, st)
                  : launch<kEpi, __nv_bfloat16, int32_t, false>(a, b, o, p, st);
@@ -1012,7 +1049,7 @@ cudaError_t launch_xent_tc(const TableProblem& p, const void* x, const void* tab
   if (!encode(&a, x, false, p.d, p.rows, planes, p.d, p.rows, kBlockK, 128) ||
       !encode(&b, table, false, p.d, p.vocab, planes, p.d, p.vocab, kBlockK, k.g.width / 2))
     return cudaErrorInvalidValue;
-  return launch_logits<Epi::kLse>(p.idx64, a, b, a, k, st);
+  return launch_logits<Epi::kLse>(p.idx64, is_fine(p), a, b, a, k, st);
 }
 
 size_t xent_tc_backward_bytes(const TableProblem& p) { return plan_backward(p).total; }
@@ -1022,8 +1059,8 @@ cudaError_t launch_xent_tc_backward(const TableProblem& p, const void* x, const 
                                     void* dx, void* dtable, void* workspace, cudaStream_t st) {
   const Backward plan = plan_backward(p);
   char* ws = static_cast<char*>(workspace);
-  const int planes = p.bf16 ? 1 : 3;
-  const bool f32 = !p.bf16;
+  const int planes = p.bf16 ? 1 : 3, g_planes = g_planes_of(p);
+  const bool f32 = !p.bf16, fine = is_fine(p);
   unsigned int* err = device_error_word();
   if (!err) return cudaErrorUnknown;
   cudaError_t e;
@@ -1057,6 +1094,7 @@ cudaError_t launch_xent_tc_backward(const TableProblem& p, const void* x, const 
     // g of the piece
     Params k = {};
     k.g = make_gemm(p.rows, nv, p.d, f32, false, false, false);
+    if (fine) k.g.chunk = kFineChunk;  // (the forward's logits, bit for bit)
     k.err = err;
     k.targets = targets;
     k.scale = p.scale;
@@ -1069,12 +1107,13 @@ cudaError_t launch_xent_tc_backward(const TableProblem& p, const void* x, const 
     // (a piece sees its own words only: rows past them read as zeros)
     if (!encode(&w_k, wv, false, p.d, nv, planes, p.d, p.vocab, kBlockK, k.g.width / 2) ||
         !encode(&w_mn, wv, false, p.d, nv, planes, p.d, p.vocab, 64, kBlockK) ||
-        !encode(&g_k, gbuf, false, nv, p.rows, planes, plan.ld, p.rows, kBlockK, 128) ||
-        !encode(&g_mn, gbuf, false, nv, p.rows, planes, plan.ld, p.rows, 64, kBlockK) ||
-        !encode(&g_out, gbuf, false, nv, p.rows, planes, plan.ld, p.rows, f32 ? 32 : 64, 32,
-                f32 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B))
+        !encode(&g_k, gbuf, false, nv, fine ? 2 * p.rows : p.rows, fine ? 1 : g_planes, plan.ld,
+                p.rows, kBlockK, 128) ||
+        !encode(&g_mn, gbuf, false, nv, p.rows, g_planes, plan.ld, p.rows, 64, kBlockK) ||
+        !encode(&g_out, gbuf, false, nv, p.rows, g_planes, plan.ld, p.rows, g_planes > 1 ? 32 : 64,
+                32, g_planes > 1 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B))
       return cudaErrorInvalidValue;
-    if ((e = launch_logits<Epi::kGrad>(p.idx64, x_k, w_k, g_out, k, st))) return e;
+    if ((e = launch_logits<Epi::kGrad>(p.idx64, fine, x_k, w_k, g_out, k, st))) return e;
     // dx += g W
     // (the first piece's cut; a last, shorter one may have blocks for fewer parts)
     Gemm gx = plan.dx;
@@ -1083,8 +1122,9 @@ cudaError_t launch_xent_tc_backward(const TableProblem& p, const void* x, const 
     gx.splits = ceil_div(gx.kb, gx.kb_split);
     gx.items = gx.m_tiles * gx.n_tiles * gx.splits;
     set_chunk(&gx);
-    if ((e = launch_product(gx, g_k, w_mn, dx_rows, plan.f32_dx, p.d, p.rows, v0 > 0, count, false,
-                            err, st)))
+    // (rows past the last one that has a target are not looked at below)
+    if ((e = launch_product(gx, g_k, w_mn, dx_rows, plan.f32_dx, p.d, fine ? 2 * p.rows : p.rows,
+                            v0 > 0, fine ? nullptr : count, false, err, st)))
       return e;
     // dW = g^T x
     Gemm gw = plan.dw;
@@ -1105,9 +1145,9 @@ cudaError_t launch_xent_tc_backward(const TableProblem& p, const void* x, const 
   }
   // dx's rows to their places
   if (f32)
-    return launch_sum<float, float>(dx_rows, dx, slots, count, p.rows, p.d, plan.dx.splits, st);
+    return launch_sum<float, float>(dx_rows, dx, slots, count, p.rows, p.d, plan.dx_planes, st);
   if (plan.f32_dx)
-    return launch_sum<float, __nv_bfloat16>(dx_rows, dx, slots, count, p.rows, p.d, plan.dx.splits,
+    return launch_sum<float, __nv_bfloat16>(dx_rows, dx, slots, count, p.rows, p.d, plan.dx_planes,
                                             st);
   return launch_sum<__nv_bfloat16, __nv_bfloat16>(dx_rows, dx, slots, count, p.rows, p.d, 1, st);
 }

@@ -174,6 +174,37 @@ def test_xent(n, vocab, d, dtype, index, scale, holes, portable):
     assert torch.equal(again[0], dx) and torch.equal(again[1], dw)
 
 
+@pytest.mark.parametrize("portable", [False, True])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("scale", [1.0, -0.5])
+@pytest.mark.parametrize("n,vocab", [(1, 700), (30, 257), (33, 1000), (128, 300), (129, 300), (700, 65)])
+def test_xent_of_sure_rows_keeps_its_digits(n, vocab, scale, dtype, portable):
+    # The target's logit is 8 to 40 above the others: the loss is exp(-8) to
+    # exp(-40), and its relative error is the logits' absolute one.
+    d = 16
+    g = gen(n + vocab)
+    t = torch.randint(0, vocab, (n,), device=DEV, generator=g)
+    table = randn(g, vocab, d, dtype=dtype)
+    lift = 8 + 32 * torch.rand(n, 1, device=DEV, generator=g)
+    own = table[t].float()
+    x = (own * lift / (own.square().sum(1, keepdim=True) * scale)).to(dtype)
+    loss, lse = lsh.lsh_attn_xent(x, table, t, scale=scale, portable=portable)
+    xd, wd = x.double(), table.double()
+    z = xd @ wd.T * scale
+    zt = z.gather(1, t[:, None])
+    rest = (z - zt).scatter(1, t[:, None], float("-inf"))
+    want = torch.logsumexp(torch.cat([rest, torch.zeros_like(zt)], 1), 1)
+    small = torch.logsumexp(rest, 1)
+    want = torch.where(small < -20, small.exp() * (1 - small.exp() / 2), want)
+    # a logit of 16 products: at most 16 + 6 roundings (planes, additions, the
+    # scale), each cut off (2^-23) of what is summed; two logits; the exponentials,
+    # sums and the logarithm: 64 more half steps
+    size = (xd.abs() @ wd.abs().T).amax(1) * abs(scale)
+    bound = want * (2 * 22 * 2.0 ** -23 * size + 64 * 2.0 ** -24) + 2.0 ** -140
+    R.check("loss", loss, (want, bound))
+    R.check("lse", lse, (want + zt[:, 0], 44 * 2.0 ** -23 * size + 2.0 ** -22 * zt[:, 0].abs() + 2.0 ** -22))
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("valid", [0, 1, 31, 32, 63, 64, 65, 97, 128, 255, 256, 257, 449, 600])
 def test_xent_backward_of_as_many_rows(valid, dtype):
@@ -191,6 +222,30 @@ def test_xent_backward_of_as_many_rows(valid, dtype):
                                        BF16 if dtype == BF16 else None)
     R.check("dx", dx, want_dx)
     R.check("dtable", dw, want_dw)
+
+
+@pytest.mark.parametrize("n,vocab,d", [(1, 700, 264), (5, 3001, 520), (64, 333, 72), (100, 2000, 136),
+                                       (128, 513, 1024)])
+def test_xent_backward_of_few_bf16_rows_rounds_once(n, vocab, d):
+    # g is held in 16 bits or more up to 128 rows: the results' own rounding is
+    # what shows.  Half a step of bfloat16 (2^-8) of each value, and 2^-14 of the
+    # sum of the products' sizes: 2^-17 for g in two planes, 2^-15 for the
+    # logits (below 2^6 in size, cut 22 times at 2^-23), the rest for the sums.
+    x, table, t, dloss = make_xent(n, vocab, d, BF16, torch.int64, 0.1)
+    lse = lsh.lsh_attn_xent(x, table, t)[1]
+    dx, dw = lsh.lsh_attn_xent_backward(x, table, t, lse, dloss)
+    xd, wd = x.double(), table.double()
+    live = (t >= 0) & (t < vocab)
+    grad = torch.softmax(xd @ wd.T, 1)
+    grad[live.nonzero()[:, 0], t[live].long()] -= 1
+    # (p - 1 of a sure target is cut off at p's size)
+    size = torch.softmax(xd @ wd.T, 1)
+    size[live.nonzero()[:, 0], t[live].long()] += 1
+    up = torch.where(live, dloss, torch.zeros_like(dloss)).double()[:, None]
+    grad, size = grad * up, size * up.abs()
+    for name, got, want, sums in (("dx", dx, grad @ wd, size @ wd.abs()),
+                                  ("dtable", dw, grad.T @ xd, size.T @ xd.abs())):
+        R.check(name, got, (want, want.abs() * 2.0 ** -8 + sums * 2.0 ** -14 + 1e-30))
 
 
 @pytest.mark.parametrize("n,vocab,d,dtype", [(20011, 14001, 24, BF16), (9001, 10007, 40, F32)])
