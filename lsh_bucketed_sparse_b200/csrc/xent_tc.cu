@@ -751,15 +751,19 @@ constexpr double kTileCycles = 3000;  // to fill and empty the pipeline
 constexpr int kPlaneChunk = 2;
 void set_chunk(Gemm* g) { g->chunk = g->planes ? kPlaneChunk : g->kb_split; }
 
-// Up to so many bfloat16 rows, where the products wait for the table and half
-// of a tile's 256 rows is empty, two things are done that more rows could not
-// pay for.  The logits' accumulators are cut every kFineChunk blocks, too (a loss
-// of one row off by 4e-6 of its logits' 15 otherwise, now 7e-7).  And g has two
-// bfloat16 planes, 16 bits of significand, which keeps its rounding out of dx and
-// dW (off by 0.0017, their own rounding; with one plane by 0.0025 to 0.004): the
-// second plane is more rows of the same tile for dx, more of a short K for dW.
+// g of bfloat16 rows is rounded to bfloat16 for its products, as a matrix that
+// is stored between two of them is: dx and dW are off by 0.0025 to 0.0028 of
+// their size, 0.0017 of which is their own rounding.  Up to kFineRows rows,
+// where the products wait for the table and half of a tile's 256 rows is empty,
+// two things are done that more rows could not pay for.  The logits'
+// accumulators are cut every kFineChunk blocks, too (the loss of a few rows was
+// off by up to 6e-6 of its size, now 1.4e-6).  And g has two bfloat16 planes, 16
+// bits of significand (dx and dW were off by up to 0.004, as one large entry's
+// rounding is not averaged out, now 0.0017): the second plane is more rows of
+// the same tile for dx, more of a short K for dW.
 // 131072 words of 1024: 16 rows 82 us forward and 223 backward (without: 76 and
 // 188), 128 rows 82 and 264 (74 and 197); 256 rows would go from 227 to 365.
+// Small problems of more rows would pay, too: 600 x 1153 x 656 backward 51 us, not 43.
 constexpr int kFineRows = 128, kFineChunk = 4;
 bool is_fine(const TableProblem& p) { return p.bf16 && p.rows <= kFineRows; }
 int g_planes_of(const TableProblem& p) { return !p.bf16 ? 3 : is_fine(p) ? 2 : 1; }
