@@ -371,6 +371,8 @@ LSH_ATTN_API lsh_status lsh_attn_embed_backward(const lsh_table* shape, const vo
  * never stored:
  *   z_iv = scale x_i . table_v,  lse_i = log sum_v exp(z_iv),
  *   loss_i = lse_i - z_i,targets_i, and 0 for padding (lse is still given).
+ * The target's exponential is kept apart from the others' sum, so that a loss
+ * far below 1 keeps its digits.
  *   x [n, D] dtype; table [V, D] dtype; targets [n] index type; loss, lse
  *   [n] float32 out.  float32 values are taken apart for the tensor cores: an
  *   infinite one makes the logits that it takes part in NaN (not so with
@@ -388,7 +390,8 @@ LSH_ATTN_API lsh_status lsh_attn_xent(const lsh_table* shape, const void* x, con
  * lse as the forward gave it.  Rows of padding get dx = 0 and take no part in
  * dtable, whatever x and dloss hold there.
  *   dx [n, D] dtype out; dtable [V, D] dtype out.  With bfloat16, g is rounded
- *   to bfloat16 before the two products; they are summed in float32.
+ *   to bfloat16 before the two products (up to 128 rows: to two of them, 16
+ *   bits); they are summed in float32.
  *   The work is that of the rows that have a target.
  *   workspace: at least lsh_attn_xent_backward_workspace_size() bytes,
  *   256-byte aligned (may be NULL when that is 0).                          */

@@ -1,6 +1,7 @@
 // Softmax cross entropy over the table's rows on CUDA cores, in float32:
 //   z_iv = scale x_i . W_v,  lse_i = log sum_v exp z_iv,
 //   loss_i = lse_i - z_i,t_i                  (0 where t_i is outside [0, V))
+//          = log1p(sum_{v != t_i} exp(z_iv - z_i,t_i)),
 //   g_iv = scale dloss_i (exp(z_iv - lse_i) - [v = t_i]),
 //   dx_i = sum_v g_iv W_v,  dW_v = sum_i g_iv x_i.
 // The logits are never stored: the forward keeps each row's running maximum

@@ -205,6 +205,21 @@ def test_xent_of_sure_rows_keeps_its_digits(n, vocab, scale, dtype, portable):
     R.check("lse", lse, (want + zt[:, 0], 44 * 2.0 ** -23 * size + 2.0 ** -22 * zt[:, 0].abs() + 2.0 ** -22))
 
 
+@pytest.mark.parametrize("portable", [False, True])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n,vocab", [(2, 40), (40, 300), (200, 777)])
+def test_xent_without_scale(n, vocab, dtype, portable):
+    # all logits are 0: log V, in a handful of float32 steps of at most 4 half ones
+    x, table, t, dloss = make_xent(n, vocab, 32, dtype, torch.int32, 0.2)
+    live = (t >= 0) & (t < vocab)
+    loss, lse = lsh.lsh_attn_xent(x, table, t, scale=0.0, portable=portable)
+    want = torch.full((n,), float(vocab), device=DEV, dtype=torch.float64).log()
+    R.check("lse", lse, (want, want * 2.0 ** -20))
+    R.check("loss", loss, (want * live, want * 2.0 ** -20))
+    dx, dw = lsh.lsh_attn_xent_backward(x, table, t, lse, dloss, scale=0.0, portable=portable)
+    assert not bool(dx.any()) and not bool(dw.any())
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("valid", [0, 1, 31, 32, 63, 64, 65, 97, 128, 255, 256, 257, 449, 600])
 def test_xent_backward_of_as_many_rows(valid, dtype):
