@@ -62,7 +62,6 @@ struct Gemm {
   int chunk;              // K blocks summed in one accumulator
   int group;              // m tiles that are walked together
   int items;
-  bool a_mn, b_mn;
 };
 
 struct Params {
@@ -164,14 +163,18 @@ __device__ __forceinline__ float ex2(float x) {
 }
 
 // T: type of D in memory; kPlanes: float32 operands in three planes each;
-// kFine: bfloat16 operands of few rows (kFineRows below).
-template <Epi kEpi, typename T, typename I, bool kPlanes, bool kFine = false>
+// kFine: bfloat16 operands of few rows (kFineRows below); kAMn: A (dW's) is
+// MN-major, as B is of both gradients.  (Descriptors are sums with constants:
+// with the layouts taken from a parameter the logits of 4093 x 131071 x 512
+// took 419 us instead of 402.)
+template <Epi kEpi, typename T, typename I, bool kPlanes, bool kFine = false, bool kAMn = false>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__ CUtensorMap bmap,
                const __grid_constant__ CUtensorMap omap, const Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  constexpr bool kBMn = kEpi == Epi::kStore || kEpi == Epi::kAdd;
   constexpr int kOps = kPlanes ? 3 : 1, kDepth = kSlots / kOps;  // slots per K block, K blocks
   uint8_t* staging = smem + kSlots * kSlotBytes;
   uint64_t* full = reinterpret_cast<uint64_t*>(staging + kEpiWarps * kStaging);  // CTA 0's
@@ -228,8 +231,8 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
     if (lane == 0) {
       tma_prefetch_desc(&amap);
       tma_prefetch_desc(&bmap);
-      const int b_boxes = g.b_mn ? (g.width / 2 + 63) / 64 : 1;
-      const uint32_t b_bytes = g.b_mn ? b_boxes * 8192 : g.width / 2 * 128;
+      const int b_boxes = kBMn ? (g.width / 2 + 63) / 64 : 1;
+      const uint32_t b_bytes = kBMn ? b_boxes * 8192 : g.width / 2 * 128;
       const uint32_t bytes = 2 * (kOperand + b_bytes);  // of both CTAs
       int n_loads = 0;
       bool ok = true;
@@ -241,8 +244,8 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
           const int c0 = n * g.width + rank * (nw / 2);
           for (int kb = it.k0; ok && kb < it.k1; ++kb, ++n_loads) {
             // two planes of A meet the same block of B one after the other
-            const int first = !kPlanes && g.a_planes == 2 ? kb & 1 : 0;
-            const int k = (!kPlanes && g.a_planes == 2 ? kb >> 1 : kb) * kBlockK;
+            const int first = kAMn && !kPlanes && g.a_planes == 2 ? kb & 1 : 0;
+            const int k = (kAMn && !kPlanes && g.a_planes == 2 ? kb >> 1 : kb) * kBlockK;
             // planes in the order in which their slots become free
 #pragma unroll
             for (int z = kOps - 1; z >= 0; --z) {
@@ -255,13 +258,13 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
               const uint32_t bar = cluster_addr(&full[s], 0);
               uint8_t* a = smem + s * kSlotBytes;
               uint8_t* b = a + kOperand;
-              if (g.a_mn) {
+              if constexpr (kAMn) {
                 tma_load_3d_pair(a, &amap, bar, m0, k, first + z);
                 tma_load_3d_pair(a + 8192, &amap, bar, m0 + 64, k, first + z);
               } else {
                 tma_load_3d_pair(a, &amap, bar, k, m0, first + z);
               }
-              if (g.b_mn) {
+              if constexpr (kBMn) {
                 for (int j = 0; j < b_boxes; ++j)
                   tma_load_3d_pair(b + j * 8192, &bmap, bar, c0 + 64 * j, k, z);
               } else {
@@ -287,8 +290,12 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
   } else if (warp == 1) {
     // -------------------------------------------------------------- MMAs
     if (rank == 0 && lane == 0) {
-      const uint32_t major = (g.a_mn ? 1u << 15 : 0u) | (g.b_mn ? 1u << 16 : 0u);
-      const uint32_t a_step = g.a_mn ? 2048 : 32, b_step = g.b_mn ? 2048 : 32;  // 16 of K
+      constexpr uint32_t major = (kAMn ? 1u << 15 : 0u) | (kBMn ? 1u << 16 : 0u);
+      // descriptors of slot 0; addresses in them count 16 bytes
+      constexpr uint32_t a_step = (kAMn ? 2048 : 32) >> 4, b_step = (kBMn ? 2048 : 32) >> 4;
+      const uint32_t a0 = smem_u32(smem), b0 = a0 + kOperand;
+      const uint64_t a_desc = kAMn ? sdesc_mn(a0) : sdesc_kmajor_sw128(a0);
+      const uint64_t b_desc = kBMn ? sdesc_mn(b0) : sdesc_kmajor_sw128(b0);
       int n_loads = 0, tile = 0;
       bool ok = true, issued = false;
       for (int item = pair; ok && item < g.items; item += pairs) {
@@ -310,15 +317,12 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
               const uint32_t parity = (n_loads / kDepth) & 1;
               // product of plane za of A and zb of B into the accumulator
               auto product = [&](int za, int zb, uint32_t accumulate) {
-                const uint32_t a = smem_u32(smem + (s0 + za) * kSlotBytes);
-                const uint32_t b = smem_u32(smem + (s0 + zb) * kSlotBytes + kOperand);
+                const uint64_t a = a_desc + (uint32_t)((s0 + za) * (kSlotBytes >> 4));
+                const uint64_t b = b_desc + (uint32_t)((s0 + zb) * (kSlotBytes >> 4));
 #pragma unroll
-                for (int k = 0; k < kBlockK / 16; ++k) {
-                  const uint32_t ak = a + k * a_step, bk = b + k * b_step;
-                  mma_bf16_ss_pair(d, g.a_mn ? sdesc_mn(ak) : sdesc_kmajor_sw128(ak),
-                                   g.b_mn ? sdesc_mn(bk) : sdesc_kmajor_sw128(bk), idesc,
+                for (int k = 0; k < kBlockK / 16; ++k)  // 16 of K
+                  mma_bf16_ss_pair(d, a + k * a_step, b + k * b_step, idesc,
                                    accumulate | (uint32_t)(k > 0));
-                }
                 issued = true;
               };
               ok = mbar_wait_for(&full[s0], parity, abort_flag,
@@ -806,8 +810,7 @@ void set_tiles(Gemm* g, bool may_split) {
   set_chunk(g);
 }
 
-Gemm make_gemm(long long rows, int cols, int k, bool f32, bool a_mn, bool b_mn, bool may_split,
-               int a_planes = 1) {
+Gemm make_gemm(long long rows, int cols, int k, bool f32, bool may_split, int a_planes = 1) {
   Gemm g = {};
   g.a_planes = a_planes;
   g.rows = (int)rows;
@@ -816,8 +819,6 @@ Gemm make_gemm(long long rows, int cols, int k, bool f32, bool a_mn, bool b_mn, 
   g.kb = ceil_div(k, kBlockK);
   g.planes = f32;
   g.group = 16;
-  g.a_mn = a_mn;
-  g.b_mn = b_mn;
   set_tiles(&g, may_split);
   return g;
 }
@@ -826,7 +827,7 @@ Gemm make_gemm(long long rows, int cols, int k, bool f32, bool a_mn, bool b_mn, 
 // partial results per row.  The longest run that costs at most 2% more time
 // than the best one.
 Gemm logits_gemm(const TableProblem& p) {
-  Gemm g = make_gemm(p.rows, p.vocab, p.d, !p.bf16, false, false, false);
+  Gemm g = make_gemm(p.rows, p.vocab, p.d, !p.bf16, false);
   const int pairs = pairs_of_device();
   auto span = [&](int run) {
     return (long long)ceil_div((long long)g.m_tiles * ceil_div(g.n_tiles, run), pairs) * run;
@@ -878,8 +879,8 @@ Backward plan_backward(const TableProblem& p) {
   b.ld = (size_t)b.words;
   const int words = std::min(b.words, p.vocab);
   // (two planes of g are twice the rows for dx, in the same tile, and twice K for dW)
-  b.dx = make_gemm(p.rows * (fine ? 2 : 1), p.d, words, !p.bf16, false, true, true);
-  b.dw = make_gemm(words, p.d, (int)p.rows, !p.bf16, true, true, true, fine ? 2 : 1);
+  b.dx = make_gemm(p.rows * (fine ? 2 : 1), p.d, words, !p.bf16, true);
+  b.dw = make_gemm(words, p.d, (int)p.rows, !p.bf16, true, fine ? 2 : 1);
   b.dx_planes = b.dx.splits * (fine ? 2 : 1);
   b.f32_dx = !p.bf16 || fine || b.dx.splits > 1 || b.pieces > 1;
   b.sum_dw = b.dw.splits > 1;
@@ -915,10 +916,10 @@ bool encode(CUtensorMap* map, const void* base, bool f32, long long cols, long l
                               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <Epi kEpi, typename T, typename I, bool kPlanes, bool kFine = false>
+template <Epi kEpi, typename T, typename I, bool kPlanes, bool kFine = false, bool kAMn = false>
 cudaError_t launch(const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& o,
                    const Params& p, cudaStream_t st) {
-  auto kernel = xent_tc_kernel<kEpi, T, I, kPlanes, kFine>;
+  auto kernel = xent_tc_kernel<kEpi, T, I, kPlanes, kFine, kAMn>;
   static std::atomic<unsigned long long> set{0};  // devices that know the size already
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -990,7 +991,8 @@ cudaError_t launch_sum(const void* sums, void* out, const int32_t* slots, const 
 }
 
 // Product into rows [0, g.rows) of out: straight into the result (splits == 1)
-// or into g.splits planes of float32 sums; `add` to what is there.
+// or into g.splits planes of float32 sums; `add` to what is there.  count_k: *count
+// is the length of K (dW), otherwise the number of rows (dx).
 cudaError_t launch_product(const Gemm& g, const CUtensorMap& a, const CUtensorMap& b, void* out,
                            bool f32, int d, long long plane_rows, bool add, const int32_t* count,
                            bool count_k, unsigned int* err, cudaStream_t st) {
@@ -1002,12 +1004,19 @@ cudaError_t launch_product(const Gemm& g, const CUtensorMap& a, const CUtensorMa
   p.err = err;
   p.count = count;
   p.count_k = count_k;
-  if (!f32) return launch<Epi::kStore, __nv_bfloat16, int32_t, false>(a, b, o, p, st);
+  constexpr Epi kStore = Epi::kStore, kAdd = Epi::kAdd;
+  using B = __nv_bfloat16;
+  if (count_k) {  // dW
+    if (!f32) return launch<kStore, B, int32_t, false, false, true>(a, b, o, p, st);
+    return g.planes ? launch<kStore, float, int32_t, true, false, true>(a, b, o, p, st)
+                    : launch<kStore, float, int32_t, false, false, true>(a, b, o, p, st);
+  }
+  if (!f32) return launch<kStore, B, int32_t, false>(a, b, o, p, st);
   if (!g.planes)
-    return add ? launch<Epi::kAdd, float, int32_t, false>(a, b, o, p, st)
-               : launch<Epi::kStore, float, int32_t, false>(a, b, o, p, st);
-  return add ? launch<Epi::kAdd, float, int32_t, true>(a, b, o, p, st)
-             : launch<Epi::kStore, float, int32_t, true>(a, b, o, p, st);
+    return add ? launch<kAdd, float, int32_t, false>(a, b, o, p, st)
+               : launch<kStore, float, int32_t, false>(a, b, o, p, st);
+  return add ? launch<kAdd, float, int32_t, true>(a, b, o, p, st)
+             : launch<kStore, float, int32_t, true>(a, b, o, p, st);
 }
 
 }  // namespace
@@ -1097,7 +1106,7 @@ cudaError_t launch_xent_tc_backward(const TableProblem& p, const void* x, const 
     const char* wv = static_cast<const char*>(w) + (size_t)v0 * p.d * 2;
     // g of the piece
     Params k = {};
-    k.g = make_gemm(p.rows, nv, p.d, f32, false, false, false);
+    k.g = make_gemm(p.rows, nv, p.d, f32, false);
     if (fine) k.g.chunk = kFineChunk;  // (the forward's logits, bit for bit)
     k.err = err;
     k.targets = targets;

@@ -263,6 +263,24 @@ def test_xent_backward_of_few_bf16_rows_rounds_once(n, vocab, d):
         R.check(name, got, (want, want.abs() * 2.0 ** -8 + sums * 2.0 ** -14 + 1e-30))
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n,valid", [(7, 0), (7, 5), (100, 0), (100, 1), (100, 33), (100, 64), (100, 65),
+                                     (128, 127)])
+def test_xent_backward_of_few_rows_with_a_target(n, valid, dtype):
+    x, table, t, dloss = make_xent(n, 530, 72, dtype, torch.int32, 0)
+    keep = torch.randperm(n, device=DEV, generator=gen(valid))[:valid]
+    targets = torch.full_like(t, 530)
+    targets[keep] = t[keep]
+    lse = lsh.lsh_attn_xent(x, table, targets)[1]
+    need = lsh.lsh_attn_xent_backward_workspace_size(lsh.make_table_shape(n, 530, 72, dtype))
+    ws = torch.full((need,), 0xff, dtype=torch.uint8, device=DEV)    # NaN everywhere
+    dx, dw = lsh.lsh_attn_xent_backward(x, table, targets, lse, dloss, workspace=ws)
+    want_dx, want_dw = R.xent_backward(x, table, targets, dloss, 1.0,
+                                       BF16 if dtype == BF16 else None)
+    R.check("dx", dx, want_dx)
+    R.check("dtable", dw, want_dw)
+
+
 @pytest.mark.parametrize("n,vocab,d,dtype", [(20011, 14001, 24, BF16), (9001, 10007, 40, F32)])
 def test_xent_backward_in_pieces(n, vocab, d, dtype):
     # more gradient values than one piece of the vocabulary holds
