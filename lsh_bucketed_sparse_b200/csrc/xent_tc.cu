@@ -83,6 +83,16 @@ struct Params {
   unsigned long long first_wait_ns;  // limit of the MMA thread's first wait for operands
 };
 
+// A place in the ring of slots: the stage and the parity of its round.
+template <int kDepth>
+struct Ring {
+  int stage = 0;
+  uint32_t phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++stage == kDepth) { stage = 0; phase ^= 1; }
+  }
+};
+
 struct Item {
   int m, n0, n1, k0, k1, split;
 };
@@ -235,6 +245,7 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
       const uint32_t b_bytes = kBMn ? b_boxes * 8192 : g.width / 2 * 128;
       const uint32_t bytes = 2 * (kOperand + b_bytes);  // of both CTAs
       int n_loads = 0;
+      Ring<kDepth> at;
       bool ok = true;
       for (int item = pair; ok && item < g.items; item += pairs) {
         const Item it = decode(g, item);
@@ -242,15 +253,15 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
         for (int n = it.n0; ok && n < it.n1; ++n) {
           const int nw = n == g.n_tiles - 1 ? g.last_width : g.width;
           const int c0 = n * g.width + rank * (nw / 2);
-          for (int kb = it.k0; ok && kb < it.k1; ++kb, ++n_loads) {
+          for (int kb = it.k0; ok && kb < it.k1; ++kb, ++n_loads, at.next()) {
             // two planes of A meet the same block of B one after the other
             const int first = kAMn && !kPlanes && g.a_planes == 2 ? kb & 1 : 0;
             const int k = (kAMn && !kPlanes && g.a_planes == 2 ? kb >> 1 : kb) * kBlockK;
             // planes in the order in which their slots become free
 #pragma unroll
             for (int z = kOps - 1; z >= 0; --z) {
-              const int s = n_loads % kDepth * kOps + z;
-              if (!mbar_wait(&empty[s], ((n_loads / kDepth) & 1) ^ 1, abort_flag)) {
+              const int s = at.stage * kOps + z;
+              if (!mbar_wait(&empty[s], at.phase ^ 1, abort_flag)) {
                 ok = false;
                 break;
               }
@@ -296,7 +307,8 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
       const uint32_t a0 = smem_u32(smem), b0 = a0 + kOperand;
       const uint64_t a_desc = kAMn ? sdesc_mn(a0) : sdesc_kmajor_sw128(a0);
       const uint64_t b_desc = kBMn ? sdesc_mn(b0) : sdesc_kmajor_sw128(b0);
-      int n_loads = 0, tile = 0;
+      int tile = 0;
+      Ring<kDepth> at;
       bool ok = true, issued = false;
       for (int item = pair; ok && item < g.items; item += pairs) {
         const Item it = decode(g, item);
@@ -312,9 +324,9 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
               break;
             }
             tc_fence_after_sync();
-            for (int kb = 0; ok && kb < blocks; ++kb, ++n_loads) {
-              const int s0 = n_loads % kDepth * kOps;
-              const uint32_t parity = (n_loads / kDepth) & 1;
+            for (int kb = 0; ok && kb < blocks; ++kb, at.next()) {
+              const int s0 = at.stage * kOps;
+              const uint32_t parity = at.phase;
               // product of plane za of A and zb of B into the accumulator
               auto product = [&](int za, int zb, uint32_t accumulate) {
                 const uint64_t a = a_desc + (uint32_t)((s0 + za) * (kSlotBytes >> 4));
@@ -326,7 +338,7 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
                 issued = true;
               };
               ok = mbar_wait_for(&full[s0], parity, abort_flag,
-                                 n_loads == 0 ? p.first_wait_ns : kWaitLimitNs);
+                                 issued ? kWaitLimitNs : p.first_wait_ns);
               if constexpr (kPlanes) {
                 ok = ok && mbar_wait(&full[s0 + 2], parity, abort_flag);
                 if (!ok) break;
