@@ -423,7 +423,8 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
       *reinterpret_cast<uint4*>(mine + lane * 128 + ((j ^ (lane & 7)) << 4)) = w;
     };
     auto put64 = [&](int j, uint4 w, int plane = 0) {
-      *reinterpret_cast<uint4*>(mine + plane * 2048 + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) = w;
+      uint8_t* row = mine + plane * 2048 + lane * 64;
+      *reinterpret_cast<uint4*>(row + ((j ^ ((lane >> 1) & 3)) << 4)) = w;
     };
     // (a vote, so that a wait that runs out ends for the whole warp)
     auto wait_tile = [&](int buf, int tile) {
