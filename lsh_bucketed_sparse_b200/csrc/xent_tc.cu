@@ -769,7 +769,7 @@ constexpr int kPlaneChunk = 2;
 void set_chunk(Gemm* g) { g->chunk = g->planes ? kPlaneChunk : g->kb_split; }
 
 // g of bfloat16 rows is rounded to bfloat16 for its products, as a matrix that
-// is stored between two of them is: dx and dW are off by 0.0025 to 0.0028 of
+// is stored between two of them is: dx and dW are off by 0.002 to 0.0032 of
 // their size, 0.0017 of which is their own rounding.  Up to kFineRows rows,
 // where the products wait for the table and half of a tile's 256 rows is empty,
 // two things are done that more rows could not pay for.  The logits'
