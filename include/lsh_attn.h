@@ -389,9 +389,9 @@ LSH_ATTN_API lsh_status lsh_attn_xent(const lsh_table* shape, const void* x, con
  *   dx_i = sum_v g_iv table_v,  dtable_v = sum_i g_iv x_i,
  * lse as the forward gave it.  Rows of padding get dx = 0 and take no part in
  * dtable, whatever x and dloss hold there.
- *   dx [n, D] dtype out; dtable [V, D] dtype out.  With bfloat16, g is rounded
- *   to bfloat16 before the two products (up to 128 rows: to two of them, 16
- *   bits); they are summed in float32.
+ *   dx [n, D] dtype out; dtable [V, D] dtype out.  With bfloat16, g is held in
+ *   two bfloat16 values, 16 bits, for the two products; they are summed in
+ *   float32 and rounded once.
  *   The work is that of the rows that have a target.
  *   workspace: at least lsh_attn_xent_backward_workspace_size() bytes,
  *   256-byte aligned (may be NULL when that is 0).                          */

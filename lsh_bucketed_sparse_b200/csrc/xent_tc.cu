@@ -57,7 +57,7 @@ struct Gemm {
   int run, slices;        // n tiles of one work item, items per m tile
   int splits, kb_split;   // K in `splits` parts of kb_split blocks
   int kb;                 // K blocks of 64
-  int a_planes;           // bf16 A: one plane or two, block by block of K
+  int a_planes;           // bf16 A (g): one plane or two, block by block of K
   bool planes;            // float32 operands
   int chunk;              // K blocks summed in one accumulator
   int group;              // m tiles that are walked together
@@ -255,8 +255,8 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
           const int c0 = n * g.width + rank * (nw / 2);
           for (int kb = it.k0; ok && kb < it.k1; ++kb, ++n_loads, at.next()) {
             // two planes of A meet the same block of B one after the other
-            const int first = kAMn && !kPlanes && g.a_planes == 2 ? kb & 1 : 0;
-            const int k = (kAMn && !kPlanes && g.a_planes == 2 ? kb >> 1 : kb) * kBlockK;
+            const bool two = kBMn && !kPlanes && g.a_planes == 2;
+            const int first = two ? kb & 1 : 0, k = (two ? kb >> 1 : kb) * kBlockK;
             // planes in the order in which their slots become free
 #pragma unroll
             for (int z = kOps - 1; z >= 0; --z) {
@@ -515,12 +515,12 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
 #pragma unroll
             for (int i = 0; i < 32; ++i) z[i] = 0.f;
           }
-          if constexpr (kFine) {
+          if constexpr (!kPlanes) {
             stage_free();
 #pragma unroll
             for (int j = 0; j < 8; ++j) put64(j & 3, pack8(z + 8 * (j & 3), j < 4), j >> 2);
             send(cc, row0, 0, 2);
-          } else if constexpr (kPlanes) {
+          } else {
 #pragma unroll
             for (int pl = 0; pl < 3; ++pl) {
               stage_free();
@@ -528,11 +528,6 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
               for (int j = 0; j < 4; ++j) put64(j, pack8(z + 8 * j, true));
               send(cc, row0, pl);
             }
-          } else {
-            if (h == 0) stage_free();
-#pragma unroll
-            for (int j = 0; j < 4; ++j) put128(4 * h + j, pack8(z + 8 * j, false));
-            if (h == 1) send(cc - 32, row0, 0);
           }
         } else if constexpr (sizeof(T) == 4) {
           stage_free();
@@ -768,22 +763,19 @@ constexpr double kTileCycles = 3000;  // to fill and empty the pipeline
 constexpr int kPlaneChunk = 2;
 void set_chunk(Gemm* g) { g->chunk = g->planes ? kPlaneChunk : g->kb_split; }
 
-// g of bfloat16 rows is rounded to bfloat16 for its products, as a matrix that
-// is stored between two of them is: dx and dW are off by 0.002 to 0.0032 of
-// their size, 0.0017 of which is their own rounding.  Up to kFineRows rows,
-// where the products wait for the table and half of a tile's 256 rows is empty,
-// two things are done that more rows could not pay for.  The logits'
-// accumulators are cut every kFineChunk blocks, too (the loss of a few rows was
-// off by up to 6e-6 of its size, now 1.4e-6).  And g has two bfloat16 planes, 16
-// bits of significand (dx and dW were off by up to 0.004, as one large entry's
-// rounding is not averaged out, now 0.0017): the second plane is more rows of
-// the same tile for dx, more of a short K for dW.
-// 131072 words of 1024: 16 rows 82 us forward and 223 backward (without: 76 and
-// 188), 128 rows 82 and 264 (74 and 197); 256 rows would go from 227 to 365.
-// Small problems of more rows would pay, too: 600 x 1153 x 656 backward 51 us, not 43.
+// g of bfloat16 rows has two bfloat16 planes, 16 bits of significand, so that what
+// shows in dx and dW is their own rounding (0.0017 of their size; with g in one
+// plane, half of the products' work, 0.002 to 0.004).  The second plane is another
+// K block of each product.
+// Up to kFineRows rows (given, those without a target among them), where the
+// products wait for the table and half of a tile's 256 rows is empty, the second
+// plane is more rows of the same tile for dx (131072 words of 1024, 16 rows: 223
+// us backward, 270 with more of K), and the logits' accumulators are cut every
+// kFineChunk blocks (the loss of a few rows was off by up to 6e-6 of its size, now
+// 1.4e-6; 82 us forward, 76 without).
 constexpr int kFineRows = 128, kFineChunk = 4;
 bool is_fine(const TableProblem& p) { return p.bf16 && p.rows <= kFineRows; }
-int g_planes_of(const TableProblem& p) { return !p.bf16 ? 3 : is_fine(p) ? 2 : 1; }
+int g_planes_of(const TableProblem& p) { return p.bf16 ? 2 : 3; }
 
 // Cuts D's columns into tiles (of a multiple of 64) and K into parts (with
 // may_split) so that the estimated time is least: fewer columns or a part of K
@@ -859,8 +851,9 @@ Gemm logits_gemm(const TableProblem& p) {
 
 // The backward's pieces: g of `words` columns (a multiple of 256) within
 // kGradBytes.  Among those, the count whose pieces take the fewest waves of
-// dW tiles, then the largest.
-constexpr size_t kGradBytes = 640u << 20;
+// dW tiles, then the largest.  (32768 x 32768 x 1024 bf16: 9.24 ms; with half of
+// the bytes, twice the pieces, 10.03.)
+constexpr size_t kGradBytes = 1280u << 20;
 struct Backward {
   int words, pieces;
   size_t ld;             // columns of g
@@ -891,9 +884,9 @@ Backward plan_backward(const TableProblem& p) {
   b.pieces = ceil_div(all, tiles);
   b.ld = (size_t)b.words;
   const int words = std::min(b.words, p.vocab);
-  // (two planes of g are twice the rows for dx, in the same tile, and twice K for dW)
-  b.dx = make_gemm(p.rows * (fine ? 2 : 1), p.d, words, !p.bf16, true);
-  b.dw = make_gemm(words, p.d, (int)p.rows, !p.bf16, true, fine ? 2 : 1);
+  // two planes of g are twice K, or for dx of few rows twice the rows, in the same tile
+  b.dx = make_gemm(p.rows * (fine ? 2 : 1), p.d, words, !p.bf16, true, p.bf16 && !fine ? 2 : 1);
+  b.dw = make_gemm(words, p.d, (int)p.rows, !p.bf16, true, p.bf16 ? 2 : 1);
   b.dx_planes = b.dx.splits * (fine ? 2 : 1);
   b.f32_dx = !p.bf16 || fine || b.dx.splits > 1 || b.pieces > 1;
   b.sum_dw = b.dw.splits > 1;
@@ -1136,16 +1129,16 @@ cudaError_t launch_xent_tc_backward(const TableProblem& p, const void* x, const 
         !encode(&g_k, gbuf, false, nv, fine ? 2 * p.rows : p.rows, fine ? 1 : g_planes, plan.ld,
                 p.rows, kBlockK, 128) ||
         !encode(&g_mn, gbuf, false, nv, p.rows, g_planes, plan.ld, p.rows, 64, kBlockK) ||
-        !encode(&g_out, gbuf, false, nv, p.rows, g_planes, plan.ld, p.rows, g_planes > 1 ? 32 : 64,
-                32, g_planes > 1 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B))
+        !encode(&g_out, gbuf, false, nv, p.rows, g_planes, plan.ld, p.rows, 32, 32,
+                CU_TENSOR_MAP_SWIZZLE_64B))
       return cudaErrorInvalidValue;
     if ((e = launch_logits<Epi::kGrad>(p.idx64, fine, x_k, w_k, g_out, k, st))) return e;
     // dx += g W
     // (the first piece's cut; a last, shorter one may have blocks for fewer parts)
     Gemm gx = plan.dx;
     gx.kb = ceil_div(nv, kBlockK);
-    gx.kb_split = ceil_div(gx.kb, plan.dx.splits);
-    gx.splits = ceil_div(gx.kb, gx.kb_split);
+    gx.kb_split = ceil_div(gx.kb * gx.a_planes, plan.dx.splits);
+    gx.splits = ceil_div(gx.kb * gx.a_planes, gx.kb_split);
     gx.items = gx.m_tiles * gx.n_tiles * gx.splits;
     set_chunk(&gx);
     // (rows past the last one that has a target are not looked at below)

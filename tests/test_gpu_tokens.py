@@ -263,6 +263,31 @@ def test_xent_backward_of_few_bf16_rows_rounds_once(n, vocab, d):
         R.check(name, got, (want, want.abs() * 2.0 ** -8 + sums * 2.0 ** -14 + 1e-30))
 
 
+@pytest.mark.parametrize("n,vocab,d,holes", [(129, 700, 264, 0), (212, 3162, 104, 0.5),
+                                             (251, 4342, 72, 0.5), (258, 863, 136, 0),
+                                             (1658, 380, 232, 0.5), (3737, 885, 840, 0.1)])
+def test_xent_backward_of_many_bf16_rows_rounds_once(n, vocab, d, holes):
+    # g in two bfloat16 planes: half a step of the first leaves 2^-8 of g, half a
+    # step of the second 2^-16.  The rest is the float32 path's bound: g from
+    # float32 logits, sums of K terms at 2 K steps (twice: two planes), and the
+    # result's own rounding.
+    x, table, t, dloss = make_xent(n, vocab, d, BF16, torch.int64, holes)
+    lse = lsh.lsh_attn_xent(x, table, t)[1]
+    dx, dw = lsh.lsh_attn_xent_backward(x, table, t, lse, dloss)
+    xd, wd = x.double(), table.double()
+    live = (t >= 0) & (t < vocab)
+    size = torch.softmax(xd @ wd.T, 1)
+    at = live.nonzero()[:, 0]
+    size[at, t[live].long()] -= 1
+    size = size.abs() * torch.where(live, dloss.abs(), torch.zeros_like(dloss)).double()[:, None]
+    want_dx, want_dw = R.xent_backward(x, table, t, dloss, 1.0)
+    for name, got, (want, bound), sums, k in (
+            ("dx", dx, want_dx, size @ wd.abs(), vocab),
+            ("dtable", dw, want_dw, size.T @ xd.abs(), n)):
+        more = (2.0 ** -16 + (2 * k + 8) * R.U) * (1 + R.half_step(BF16)) * sums
+        R.check(name, got, (want, bound + more))
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("n,valid", [(7, 0), (7, 5), (100, 0), (100, 1), (100, 33), (100, 64), (100, 65),
                                      (128, 127)])
