@@ -381,6 +381,21 @@ __device__ __forceinline__ void raise_flag_cluster(const int* flag, uint32_t ran
                : "memory");
 }
 
+// The int at this place in CTA `rank` of the cluster.
+__device__ __forceinline__ int load_cluster(const int* p, uint32_t rank) {
+  int v;
+  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(cluster_addr(p, rank))
+               : "memory");
+  return v;
+}
+
+// Counts bytes on a barrier of this CTA that no copy will bring.
+__device__ __forceinline__ void mbar_complete_tx(uint64_t* bar, uint32_t bytes) {
+  asm volatile("mbarrier.complete_tx.relaxed.cta.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(bar)),
+               "r"(bytes)
+               : "memory");
+}
+
 // A tile to this CTA's shared memory, counted on a barrier of either CTA of
 // the pair (address of the cluster).
 __device__ __forceinline__ void tma_load_3d_pair(void* dst, const CUtensorMap* map,

@@ -194,6 +194,7 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
   uint64_t* done = t_empty + 2;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* loads = reinterpret_cast<int*>(tmem_slot + 2);  // that this CTA's loader has issued
   // A wait ran out: every role of both CTAs leaves its loop.
   auto give_up = [&](unsigned int code) {
     atomicOr(p.err, code);
@@ -236,15 +237,14 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
     }
   }
 
+  const int b_boxes = kBMn ? (g.width / 2 + 63) / 64 : 1;
+  const uint32_t slot_bytes = kOperand + (kBMn ? b_boxes * 8192 : g.width / 2 * 128);
   if (warp == 0) {
     // -------------------------------------------------------------- loads
     if (lane == 0) {
       tma_prefetch_desc(&amap);
       tma_prefetch_desc(&bmap);
-      const int b_boxes = kBMn ? (g.width / 2 + 63) / 64 : 1;
-      const uint32_t b_bytes = kBMn ? b_boxes * 8192 : g.width / 2 * 128;
-      const uint32_t bytes = 2 * (kOperand + b_bytes);  // of both CTAs
-      int n_loads = 0;
+      int issued = 0;  // slots filled, kOps to a K block
       Ring<kDepth> at;
       bool ok = true;
       for (int item = pair; ok && item < g.items; item += pairs) {
@@ -253,7 +253,7 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
         for (int n = it.n0; ok && n < it.n1; ++n) {
           const int nw = n == g.n_tiles - 1 ? g.last_width : g.width;
           const int c0 = n * g.width + rank * (nw / 2);
-          for (int kb = it.k0; ok && kb < it.k1; ++kb, ++n_loads, at.next()) {
+          for (int kb = it.k0; ok && kb < it.k1; ++kb, at.next()) {
             // two planes of A meet the same block of B one after the other
             const bool two = kBMn && !kPlanes && g.a_planes == 2;
             const int first = two ? kb & 1 : 0, k = (two ? kb >> 1 : kb) * kBlockK;
@@ -265,7 +265,7 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
                 ok = false;
                 break;
               }
-              if (rank == 0) mbar_arrive_expect_tx(&full[s], bytes);
+              if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * slot_bytes);  // both CTAs'
               const uint32_t bar = cluster_addr(&full[s], 0);
               uint8_t* a = smem + s * kSlotBytes;
               uint8_t* b = a + kOperand;
@@ -281,22 +281,13 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
               } else {
                 tma_load_3d_pair(b, &bmap, bar, k, c0, z);
               }
+              ++issued;
             }
           }
         }
       }
       if (!ok) give_up(kErrWaitProducer);
-      // The last loads must land before either CTA may exit (CTA 1 waits for
-      // CTA 0 at the end).
-      if (rank == 0) {
-        const unsigned long long t0 = globaltimer();
-        bool landed = true;
-        for (int l = n_loads > kDepth ? n_loads - kDepth : 0; landed && l < n_loads; ++l)
-          for (int z = 0; landed && z < kOps; ++z)
-            while (landed && !mbar_try_wait(&full[l % kDepth * kOps + z], (l / kDepth) & 1))
-              landed = globaltimer() - t0 <= kWaitLimitNs;
-        if (!landed) atomicOr(p.err, kErrWaitDrain);
-      }
+      *loads = issued;
     }
   } else if (warp == 1) {
     // -------------------------------------------------------------- MMAs
@@ -632,6 +623,29 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
   __syncwarp();
   tc_fence_before_sync();
   cluster_sync();
+  // Every load has met its product, unless a wait ran out (which both CTAs
+  // know of by now): then neither CTA may exit before the last loads of both
+  // have landed.  A slot that only one CTA has filled completes without the
+  // other's bytes.
+  if (*abort_flag) {
+    if (rank == 0 && threadIdx.x == 0) {
+      const int mine = *loads, other = load_cluster(loads, 1), last = max(mine, other);
+      const unsigned long long t0 = globaltimer();
+      bool landed = true;
+      // (the slots of earlier ones have been filled again, so they were used)
+      for (int j = max(0, last - kSlots); landed && j < last; ++j) {
+        const int block = j / kOps;
+        uint64_t* bar = &full[block % kDepth * kOps + kOps - 1 - j % kOps];
+        if (j >= mine) mbar_arrive_expect_tx(bar, slot_bytes);
+        if (j >= other) mbar_complete_tx(bar, slot_bytes);
+        while (landed && !mbar_try_wait(bar, (block / kDepth) & 1))
+          landed = globaltimer() - t0 <= kWaitLimitNs;
+      }
+      if (!landed) atomicOr(p.err, kErrWaitDrain);
+    }
+    __syncwarp();
+    cluster_sync();
+  }
   tc_fence_after_sync();
   if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }

@@ -496,6 +496,36 @@ def test_xent_wait_that_runs_out_reports_timeout_and_next_call_is_clean(dtype):
     R.check("dtable", dw, want_dw)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n,vocab,d", [(700, 900, 1024), (700, 90000, 264), (60, 900, 1024)])
+def test_xent_wait_that_runs_out_while_loads_wait_for_a_slot(n, vocab, d, dtype):
+    # more blocks of D than the ring of operands holds, or several tiles to a
+    # pair: the loaders stand before a full ring when the wait gives up.  What
+    # they have issued lands well within the limit of that second wait (bit 3).
+    x, table, t, dloss = make_xent(n, vocab, d, dtype, torch.int64, 0)
+    want = lsh.lsh_attn_xent(x, table, t)
+    want_grads = lsh.lsh_attn_xent_backward(x, table, t, want[1], dloss)
+    lib = lsh.lib()
+    lsh.lsh_attn_device_check()
+    for call in (lambda: lsh.lsh_attn_xent(x, table, t),
+                 lambda: lsh.lsh_attn_xent_backward(x, table, t, want[1], dloss)):
+        prev = lib.lsh_attn_test_xent_first_wait(0)
+        try:
+            call()
+            with pytest.raises(lsh.LshError, match="code 0x") as err:
+                lsh.lsh_attn_device_check()
+        finally:
+            assert lib.lsh_attn_test_xent_first_wait(prev) == 0
+        assert err.value.status == 5  # LSH_ERR_DEVICE_TIMEOUT
+        code = int(str(err.value).split("code ")[1].rstrip(")"), 16)
+        assert code & 2 and not code & 8, hex(code)
+    loss, lse = lsh.lsh_attn_xent(x, table, t)
+    grads = lsh.lsh_attn_xent_backward(x, table, t, lse, dloss)
+    lsh.lsh_attn_device_check()
+    for got, ref in zip((loss, lse, *grads), (*want, *want_grads)):
+        assert torch.equal(got, ref)
+
+
 # ---- routing ---------------------------------------------------------------------
 ROUTE = [  # tokens, k, experts, d, dtype, index, dropped
     (0, 2, 4, 16, BF16, torch.int64, 0),
