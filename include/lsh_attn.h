@@ -511,6 +511,14 @@ LSH_ATTN_API unsigned long long lsh_attn_test_hash_first_wait(unsigned long long
  * operands of every launch of it. */
 LSH_ATTN_API unsigned long long lsh_attn_test_xent_first_wait(unsigned long long ns);
 
+/* Test hook: the most bytes of the gradient's matrix that a piece of the
+ * vocabulary may take in the cross entropy's backward (at least one tile of
+ * it), for the calls and size queries that follow, so that a small case runs
+ * the pieces of a large one.  Limits above the library's own change nothing.
+ * Returns the previous limit.  Process-wide; not for use while other threads
+ * call. */
+LSH_ATTN_API unsigned long long lsh_attn_test_xent_piece_bytes(unsigned long long bytes);
+
 #ifdef __cplusplus
 }
 #endif

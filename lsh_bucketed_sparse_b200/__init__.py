@@ -123,6 +123,7 @@ _SIGS = {
     "lsh_attn_kernel_launches": [],
     "lsh_attn_test_hash_first_wait": [ctypes.c_ulonglong],
     "lsh_attn_test_xent_first_wait": [ctypes.c_ulonglong],
+    "lsh_attn_test_xent_piece_bytes": [ctypes.c_ulonglong],
 }
 
 
@@ -143,6 +144,7 @@ def lib() -> ctypes.CDLL:
         L.lsh_attn_kernel_launches.restype = ctypes.c_ulonglong
         L.lsh_attn_test_hash_first_wait.restype = ctypes.c_ulonglong
         L.lsh_attn_test_xent_first_wait.restype = ctypes.c_ulonglong
+        L.lsh_attn_test_xent_piece_bytes.restype = ctypes.c_ulonglong
         _lib = L
     return _lib
 

@@ -273,4 +273,8 @@ unsigned long long lsh_attn_test_xent_first_wait(unsigned long long ns) {
   return set_xent_first_wait_ns(ns);
 }
 
+unsigned long long lsh_attn_test_xent_piece_bytes(unsigned long long bytes) {
+  return set_xent_piece_bytes(bytes);
+}
+
 }  // extern "C"

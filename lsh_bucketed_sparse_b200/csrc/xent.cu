@@ -1,5 +1,8 @@
 // Cross entropy over the vocabulary: kernel choice, workspaces, and the last
 // step of the forward (each row's slices joined into lse and loss).
+#include <algorithm>
+#include <atomic>
+
 #include "common.cuh"
 #include "internal.h"
 #include "xent.cuh"
@@ -70,6 +73,9 @@ xent_clean_kernel(const uint4* __restrict__ x, const I* __restrict__ targets,
   clean[p] = target_of(targets, p / per_row, vocab) >= 0 ? x[p] : make_uint4(0, 0, 0, 0);
 }
 
+// lsh_attn_test_xent_piece_bytes sets it, so that small cases have several pieces.
+std::atomic<unsigned long long> g_piece_bytes{~0ull};
+
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 int slices_of(const TableProblem& p) {
@@ -78,6 +84,14 @@ int slices_of(const TableProblem& p) {
 }
 
 }  // namespace
+
+size_t xent_piece_bytes(size_t most) {
+  return std::min<unsigned long long>(most, g_piece_bytes.load(std::memory_order_relaxed));
+}
+
+unsigned long long set_xent_piece_bytes(unsigned long long bytes) {
+  return g_piece_bytes.exchange(bytes);
+}
 
 cudaError_t launch_xent_clean(const TableProblem& p, const void* x, const void* targets,
                               void* clean, cudaStream_t st) {

@@ -36,6 +36,10 @@ cudaError_t launch_xent_clean(const TableProblem& p, const void* x, const void* 
 // log2, or from the tensor cores as the product left it, without scale (where
 // scale is 0 the sum has it too).
 
+// Most bytes of g in a piece of the backward: `most`, or less by the test hook.
+size_t xent_piece_bytes(size_t most);
+unsigned long long set_xent_piece_bytes(unsigned long long bytes);  // returns the previous limit
+
 // ---- tensor cores (xent_tc.cu) ---------------------------------------------------
 bool xent_tc_supported(const TableProblem& p);
 // Sets the limit of the MMA thread's first wait (test hook); returns the

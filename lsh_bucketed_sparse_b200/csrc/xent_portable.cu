@@ -183,7 +183,7 @@ int slice_of(const TableProblem& p) {
 
 // Columns of a backward piece: g within 64 MB.
 int piece_of(const TableProblem& p) {
-  long long c = (64ll << 20) / (p.rows * 4) / kT * kT;
+  long long c = (long long)xent_piece_bytes(64 << 20) / (p.rows * 4) / kT * kT;
   if (c < kT) c = kT;
   const long long all = (long long)tiles_of(p.vocab) * kT;
   return (int)(c < all ? c : all);

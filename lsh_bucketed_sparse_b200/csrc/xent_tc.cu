@@ -883,7 +883,7 @@ Backward plan_backward(const TableProblem& p) {
   const bool fine = is_fine(p);
   const int all = ceil_div(p.vocab, kTileM), nt = ceil_div(p.d, kTileN);
   const size_t per_tile = (size_t)g_planes * p.rows * kTileM * 2;
-  const int most = (int)std::min<size_t>(all, std::max<size_t>(1, kGradBytes / per_tile));
+  const int most = (int)std::min<size_t>(all, std::max<size_t>(1, xent_piece_bytes(kGradBytes) / per_tile));
   int tiles = most;
   if (most < all) {
     long long best = -1;

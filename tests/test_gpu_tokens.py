@@ -319,6 +319,49 @@ def test_xent_backward_in_pieces(n, vocab, d, dtype):
     assert torch.equal(again[0], dx) and torch.equal(again[1], dw)
 
 
+PIECES = [  # rows, vocab, d, dtype, bytes of g, pieces, portable
+    # tiles of 256 words, rows x 512 bytes each in every plane of g: 2 (bf16), 3 (float32)
+    (300, 2100, 72, BF16, 2 * 2 * 300 * 512, 5, False),     # 2 + 2 + 2 + 2 + 1 tiles
+    (300, 2049, 264, BF16, 2 * 2 * 300 * 512, 5, False),    # one word in the last piece
+    (129, 1100, 136, BF16, 0, 5, False),                    # a tile each
+    (100, 2100, 72, BF16, 2 * 2 * 100 * 512, 5, False),     # few rows
+    (9001, 1100, 1032, BF16, 0, 5, False),                  # dx in whole sums over a piece
+    (300, 2100, 72, F32, 2 * 3 * 300 * 512, 5, False),
+    (33, 2049, 520, F32, 2 * 3 * 33 * 512, 5, False),
+    (4001, 1100, 1032, F32, 0, 5, False),
+    (50, 300, 72, BF16, 50 * 4 * 64, 5, True),              # 64 columns each, the last of 44
+    (70, 257, 40, F32, 0, 5, True),
+]
+
+
+@pytest.mark.parametrize("n,vocab,d,dtype,limit,pieces,portable", PIECES)
+def test_xent_backward_in_several_pieces(n, vocab, d, dtype, limit, pieces, portable):
+    # the last piece is shorter, and has fewer blocks than the first has parts of K
+    x, table, t, dloss = make_xent(n, vocab, d, dtype, torch.int64, 0.1)
+    t[:3] = torch.tensor([0, vocab - 1, vocab - 2], device=DEV)
+    lse = lsh.lsh_attn_xent(x, table, t, scale=0.5, portable=portable)[1]
+    whole = lsh.lsh_attn_xent_backward(x, table, t, lse, dloss, scale=0.5, portable=portable)
+    lib = lsh.lib()
+    before = lib.lsh_attn_test_xent_piece_bytes(limit)
+    try:
+        launches = lib.lsh_attn_kernel_launches()
+        dx, dw = lsh.lsh_attn_xent_backward(x, table, t, lse, dloss, scale=0.5, portable=portable)
+        launches = lib.lsh_attn_kernel_launches() - launches
+        again = lsh.lsh_attn_xent_backward(x, table, t, lse, dloss, scale=0.5, portable=portable)
+    finally:
+        assert lib.lsh_attn_test_xent_piece_bytes(before) == limit
+    lsh.lsh_attn_device_check()
+    # once: order, rows, table planes (float32), dx's rows; or the cleaned rows.
+    # A piece: g, dx, dW, and dW's sum where its K is in parts.
+    once = 1 if portable else 3 + (dtype == F32)
+    assert launches - once in (3 * pieces, 4 * pieces)
+    want_dx, want_dw = R.xent_backward(x, table, t, dloss, 0.5, BF16 if dtype == BF16 else None)
+    for got in ((dx, dw), whole):
+        R.check("dx", got[0], want_dx)
+        R.check("dtable", got[1], want_dw)
+    assert torch.equal(again[0], dx) and torch.equal(again[1], dw)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_xent_of_no_rows(dtype):
     x, table = torch.empty(0, 16, device=DEV, dtype=dtype), randn(gen(0), 9, 16, dtype=dtype)
