@@ -388,7 +388,7 @@ LSH_ATTN_API lsh_status lsh_attn_xent(const lsh_table* shape, const void* x, con
  *   g_iv = scale dloss_i (exp(z_iv - lse_i) - [v == targets_i]),
  *   dx_i = sum_v g_iv table_v,  dtable_v = sum_i g_iv x_i,
  * lse as the forward gave it.  Rows of padding get dx = 0 and take no part in
- * dtable, whatever x and dloss hold there.
+ * dtable, whatever x and dloss hold there and the table anywhere.
  *   dx [n, D] dtype out; dtable [V, D] dtype out.  With bfloat16, g is held in
  *   two bfloat16 values, 16 bits, for the two products; they are summed in
  *   float32 and rounded once.

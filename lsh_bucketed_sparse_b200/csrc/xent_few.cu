@@ -240,11 +240,13 @@ xent_few_grad_kernel(const Rows p, float* __restrict__ dx, float* __restrict__ d
 }
 
 // dx = the parts' sums in order: a block adds 32 float4 pieces, each warp every
-// kSumWarps-th part, then the warps' sums.
+// kSumWarps-th part, then the warps' sums.  Rows without a target are zero,
+// whatever the table holds (0 times an infinite word is NaN in the parts).
 constexpr int kSumWarps = 8;
+template <typename I>
 __global__ void __launch_bounds__(kSumWarps * 32)
-xent_few_sum_kernel(const float4* __restrict__ parts, float4* __restrict__ dx, int pieces,
-                    int n_parts) {
+xent_few_sum_kernel(const float4* __restrict__ parts, const I* __restrict__ targets,
+                    float4* __restrict__ dx, int pieces, int n_parts, int per_row, int vocab) {
   __shared__ float4 sums[kSumWarps][32];
   wait_prior_grid();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, piece = blockIdx.x * 32 + lane;
@@ -264,6 +266,7 @@ xent_few_sum_kernel(const float4* __restrict__ parts, float4* __restrict__ dx, i
     const float4 v = sums[q][lane];
     a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
   }
+  if (target_of(targets, piece / per_row, vocab) < 0) a = make_float4(0.f, 0.f, 0.f, 0.f);
   dx[piece] = a;
 }
 
@@ -315,7 +318,8 @@ cudaError_t logits(const TableProblem& p, const Rows& r, cudaStream_t st) {
 }
 
 template <typename I>
-cudaError_t grads(const TableProblem& p, const Rows& r, float* dx, float* dtable, cudaStream_t st) {
+cudaError_t grads(const TableProblem& p, const Rows& r, float* parts, float* dx, float* dtable,
+                  cudaStream_t st) {
   const int rows = padded_rows(p), per_block = kGradThreads * columns_of(rows);
   const dim3 grid(grad_parts(p), (p.d + per_block - 1) / per_block);
   auto kernel = rows == 4    ? xent_few_grad_kernel<4, I>
@@ -323,7 +327,14 @@ cudaError_t grads(const TableProblem& p, const Rows& r, float* dx, float* dtable
                 : rows == 16 ? xent_few_grad_kernel<16, I>
                              : xent_few_grad_kernel<32, I>;
   cudaError_t e =
-      launch_dependent(kernel, grid, dim3(kGradThreads), 0, st, r, dx, dtable, part_words(p));
+      launch_dependent(kernel, grid, dim3(kGradThreads), 0, st, r, parts, dtable, part_words(p));
+  if (e) return e;
+  note_launch();
+  const int pieces = (int)(p.rows * p.d / 4);
+  e = launch_dependent(xent_few_sum_kernel<I>, dim3((pieces + 31) / 32), dim3(kSumWarps * 32), 0,
+                       st, reinterpret_cast<const float4*>(parts),
+                       static_cast<const I*>(r.targets), reinterpret_cast<float4*>(dx), pieces,
+                       grad_parts(p), p.d / 4, p.vocab);
   if (e == cudaSuccess) note_launch();
   return e;
 }
@@ -374,15 +385,9 @@ cudaError_t launch_xent_few_backward(const TableProblem& p, const void* x, const
       align256((size_t)p.vocab * padded_rows(p) * sizeof(float)));
   cudaError_t e = p.idx64 ? logits<true, int64_t>(p, r, st) : logits<true, int32_t>(p, r, st);
   if (e) return e;
-  e = p.idx64 ? grads<int64_t>(p, r, parts, static_cast<float*>(dtable), st)
-              : grads<int32_t>(p, r, parts, static_cast<float*>(dtable), st);
-  if (e) return e;
-  const int pieces = (int)(p.rows * p.d / 4);
-  e = launch_dependent(xent_few_sum_kernel, dim3((pieces + 31) / 32), dim3(kSumWarps * 32), 0, st,
-                       reinterpret_cast<const float4*>(parts), static_cast<float4*>(dx), pieces,
-                       grad_parts(p));
-  if (e == cudaSuccess) note_launch();
-  return e;
+  float *to = static_cast<float*>(dx), *dw = static_cast<float*>(dtable);
+  return p.idx64 ? grads<int64_t>(p, r, parts, to, dw, st)
+                 : grads<int32_t>(p, r, parts, to, dw, st);
 }
 
 }  // namespace lsh

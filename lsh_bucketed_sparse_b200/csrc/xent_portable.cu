@@ -147,11 +147,12 @@ xent_g_kernel(const Operand<T> x, const Operand<T> w, const I* __restrict__ targ
 }
 
 // Grid (row tiles, column tiles).  out = A B^T (+ sum, a float32 matrix of
-// earlier pieces); to `out` when it is not NULL, else back to `sum`.
-template <typename TA, typename TB, typename TO>
+// earlier pieces); to `out` when it is not NULL, else back to `sum`.  With
+// `targets`, rows that have none are zero in `out`, whatever the table holds.
+template <typename TA, typename TB, typename TO, typename I>
 __global__ void __launch_bounds__(kThreads)
 xent_product_kernel(const Operand<TA> A, const Operand<TB> B, float* sum, int first, TO* out,
-                    size_t ld) {
+                    size_t ld, const I* __restrict__ targets, int vocab) {
   __shared__ Tiles s;
   wait_prior_grid();
   const int m0 = blockIdx.x * kT, n0 = blockIdx.y * kT;
@@ -166,8 +167,8 @@ xent_product_kernel(const Operand<TA> A, const Operand<TB> B, float* sum, int fi
       if (r >= A.rows || c >= B.rows) continue;
       const size_t at = (size_t)r * ld + c;
       const float v = first ? acc[i][j] : sum[at] + acc[i][j];
-      if (out) out[at] = from_f32<TO>(v);
-      else sum[at] = v;
+      if (!out) sum[at] = v;
+      else out[at] = from_f32<TO>(targets && target_of(targets, r, vocab) < 0 ? 0.f : v);
     }
 }
 
@@ -226,14 +227,16 @@ cudaError_t bwd_t(const TableProblem& p, const void* x, const void* table, const
     if (e) return e;
     note_launch();
     const bool last = v0 + piece >= p.vocab;
-    e = launch_dependent(xent_product_kernel<float, T, T>, dim3(tiles_of(n), tiles_of(p.d)),
+    e = launch_dependent(xent_product_kernel<float, T, T, I>, dim3(tiles_of(n), tiles_of(p.d)),
                          dim3(kThreads), 0, st, G, Wt, sum, (int)(v0 == 0),
-                         last ? static_cast<T*>(dx) : static_cast<T*>(nullptr), (size_t)p.d);
+                         last ? static_cast<T*>(dx) : static_cast<T*>(nullptr), (size_t)p.d,
+                         static_cast<const I*>(targets), p.vocab);
     if (e) return e;
     note_launch();
-    e = launch_dependent(xent_product_kernel<float, T, T>, dim3(tiles_of(nv), tiles_of(p.d)),
+    e = launch_dependent(xent_product_kernel<float, T, T, I>, dim3(tiles_of(nv), tiles_of(p.d)),
                          dim3(kThreads), 0, st, Gt, Xt, static_cast<float*>(nullptr), 1,
-                         static_cast<T*>(dtable) + (size_t)v0 * p.d, (size_t)p.d);
+                         static_cast<T*>(dtable) + (size_t)v0 * p.d, (size_t)p.d,
+                         static_cast<const I*>(nullptr), p.vocab);
     if (e) return e;
     note_launch();
   }

@@ -409,6 +409,18 @@ def test_few_rows_of_padding_may_hold_anything(n):
     R.check("dtable", dw, want_dw)
 
 
+@pytest.mark.parametrize("portable", [False, True])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("n", [3, 7, 16, 20, 33, 200])
+def test_padding_rows_next_to_infinite_words_have_no_gradient(n, dtype, portable):
+    x, table, t, dloss = make_xent(n, 300, 72, dtype, torch.int32, 0)
+    table[11, 3], table[250, 70] = -float("inf"), float("inf")
+    t[1::2] = 300
+    lse = lsh.lsh_attn_xent(x, table, t, portable=portable)[1]
+    dx, _ = lsh.lsh_attn_xent_backward(x, table, t, lse, dloss, portable=portable)
+    assert not bool(dx[1::2].any())
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_far_logits_do_not_overflow(dtype):
     # logits of some +-12000: exp of any of them alone is 0 or infinite
