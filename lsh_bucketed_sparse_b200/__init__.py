@@ -627,7 +627,8 @@ def lsh_attn_xent(x, table, targets, *, scale=1.0, workspace=None, portable=Fals
     shp = _xent_args(x, table, targets, scale, portable)
     with _launching(x.device, stream) as st:
         need = lsh_attn_xent_workspace_size(shp)
-        loss, lse = x.new_empty((2, *targets.shape), dtype=torch.float32).unbind(0)
+        loss = x.new_empty(targets.shape, dtype=torch.float32)
+        lse = torch.empty_like(loss)
         ws, n = _workspace(workspace, need, x)
         _check(lib().lsh_attn_xent(ctypes.byref(shp), _at(x), _at(table), _at(targets), _at(loss),
                                    _at(lse), _at(ws), n, st))

@@ -525,6 +525,19 @@ def test_xent_of_any_leading_shape_and_a_slice_of_targets():
     assert torch.equal(dx.view(-1, 64), want[0]) and torch.equal(dw, want[1])
 
 
+def test_loss_and_lse_are_tensors_of_their_own():
+    # the loss may be weighted in place with weights that have a gradient, and
+    # keeping one of the two does not keep the other's memory
+    x, table, t, _ = make_xent(20, 50, 16, F32, torch.int64, 0)
+    loss, lse = lsh.lsh_attn_xent(x, table, t)
+    assert loss.untyped_storage().nbytes() == lse.untyped_storage().nbytes() == 20 * 4
+    value, kept = loss.clone(), lse.clone()
+    w = torch.rand(20, device=DEV, requires_grad=True)
+    loss.mul_(w)
+    loss.sum().backward()
+    assert torch.equal(w.grad, value) and torch.equal(lse, kept)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_xent_wait_that_runs_out_reports_timeout_and_next_call_is_clean(dtype):
     # the first wait gives up at once, before any product is issued: both CTAs
