@@ -488,15 +488,23 @@ def _index_code(t: torch.Tensor, name: str) -> int:
     raise TypeError(f"{name} must be int32 or int64, got {t.dtype}")
 
 
+def _int32(name: str, value: int) -> int:
+    """ctypes keeps the low 32 bits of what does not fit."""
+    if not -0x80000000 <= value <= 0x7fffffff:
+        raise ValueError(f"{name}={value}: does not fit 32 bits")
+    return value
+
+
 def make_table_shape(rows, vocab, d_model, dtype=torch.bfloat16, index_type=I64, scale=1.0,
                      portable=False) -> TableShape:
-    return TableShape(rows, vocab, d_model, dtype if isinstance(dtype, int) else _dtype_code(dtype),
-                      index_type, scale, FLAG_PORTABLE if portable else 0)
+    return TableShape(rows, _int32("vocab", vocab), _int32("d_model", d_model),
+                      dtype if isinstance(dtype, int) else _dtype_code(dtype), index_type, scale, FLAG_PORTABLE if portable else 0)
 
 
 def make_route_shape(tokens, top_k, n_experts, d_model=8, dtype=torch.bfloat16,
                      index_type=I64) -> RouteShape:
-    return RouteShape(tokens, top_k, n_experts, d_model,
+    return RouteShape(tokens, _int32("top_k", top_k), _int32("n_experts", n_experts),
+                      _int32("d_model", d_model),
                       dtype if isinstance(dtype, int) else _dtype_code(dtype), index_type, 0)
 
 

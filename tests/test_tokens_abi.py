@@ -196,6 +196,20 @@ def test_binding_refuses_host_tensors_and_wrong_ranks():
             call()
 
 
+@pytest.mark.parametrize("wide", [(1 << 32) + 8, -(1 << 32) + 8, 1 << 31])
+@pytest.mark.parametrize("make,names", [
+    (lsh.make_table_shape, ("rows", "vocab", "d_model")),
+    (lsh.make_route_shape, ("tokens", "top_k", "n_experts", "d_model"))])
+def test_sizes_beyond_32_bits_do_not_wrap(make, names, wide):
+    # the sizes of the C structure are 32 bits wide, but for the first
+    for name in names[1:]:
+        sizes = dict.fromkeys(names, 8)
+        assert getattr(make(**sizes), name) == 8
+        sizes[name] = wide
+        with pytest.raises(ValueError, match=f"{name}={wide}"):
+            make(**sizes)
+
+
 def test_binding_index_types():
     with pytest.raises(TypeError, match="int32 or int64"):
         lsh._index_code(torch.zeros(2, dtype=torch.int16), "tokens")
