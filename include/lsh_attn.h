@@ -29,6 +29,8 @@
  *  - Every device pointer must be 16-byte aligned; of the token table's and
  *    the routing calls' vectors (one value per token or entry) only aligned
  *    to their values.  Tensors are dense, row-major, last dimension fastest.
+ *    Outputs and workspaces share no memory with one another or with an input,
+ *    unless a call says so.
  *  - `stream` is a cudaStream_t passed as void* (NULL = the legacy default
  *    stream).  All work is enqueued on it; no call synchronises the host
  *    except lsh_attn_device_check().

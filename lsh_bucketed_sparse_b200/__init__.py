@@ -498,7 +498,8 @@ def _int32(name: str, value: int) -> int:
 def make_table_shape(rows, vocab, d_model, dtype=torch.bfloat16, index_type=I64, scale=1.0,
                      portable=False) -> TableShape:
     return TableShape(rows, _int32("vocab", vocab), _int32("d_model", d_model),
-                      dtype if isinstance(dtype, int) else _dtype_code(dtype), index_type, scale, FLAG_PORTABLE if portable else 0)
+                      dtype if isinstance(dtype, int) else _dtype_code(dtype), index_type, scale,
+                      FLAG_PORTABLE if portable else 0)
 
 
 def make_route_shape(tokens, top_k, n_experts, d_model=8, dtype=torch.bfloat16,
@@ -555,10 +556,24 @@ def _workspace(workspace, need, like):
     return like.new_empty(need, dtype=torch.uint8), need
 
 
-def _out(t, name, dtype, shape, like):
+def _apart(out, name, **inputs):
+    """Refuses an output that shares memory with an input: threads read the one
+    while others write the other."""
+    lo, size = out.data_ptr(), out.numel() * out.element_size()
+    for of, t in inputs.items():
+        if t is None or size == 0 or t.numel() == 0:
+            continue
+        at = t.data_ptr()
+        if at < lo + size and lo < at + t.numel() * t.element_size():
+            raise ValueError(f"{name} lies over {of}")
+
+
+def _out(t, name, dtype, shape, like, **inputs):
     if t is None:
         return like.new_empty(shape, dtype=dtype)
-    return _cuda(t, name, dtype, shape, like)
+    _cuda(t, name, dtype, shape, like)
+    _apart(t, name, **inputs)
+    return t
 
 
 def _table(table, d=None, like=None):
@@ -577,7 +592,8 @@ def lsh_attn_embed(tokens, table, *, scale=1.0, out=None, stream=None):
     V, D = _table(table, None, tokens)
     shp = make_table_shape(tokens.numel(), V, D, table.dtype, _index_code(tokens, "tokens"), scale)
     with _launching(tokens.device, stream) as st:
-        out = _out(out, "out", table.dtype, (*tokens.shape, D), tokens)
+        out = _out(out, "out", table.dtype, (*tokens.shape, D), tokens, tokens=tokens,
+                   table=table)
         _check(lib().lsh_attn_embed(ctypes.byref(shp), _at(tokens), _at(table), _at(out), st))
     return out
 
@@ -604,7 +620,10 @@ def lsh_attn_embed_backward(tokens, dout, vocab, *, scale=1.0, init=None, out=No
                            scale)
     with _launching(tokens.device, stream) as st:
         need = lsh_attn_embed_backward_workspace_size(shp)
-        out = _out(out, "out", dout.dtype, (vocab, D), tokens)
+        # (init may be out itself: each row is read before it is written)
+        over = out is not None and init is not None and init.data_ptr() == out.data_ptr()
+        out = _out(out, "out", dout.dtype, (vocab, D), tokens, tokens=tokens, dout=dout,
+                   init=None if over else init)
         ws, n = _workspace(workspace, need, tokens)
         _check(lib().lsh_attn_embed_backward(ctypes.byref(shp), _at(tokens), _at(dout), _at(init),
                                              _at(out), _at(ws), n, st))
@@ -711,7 +730,8 @@ def lsh_attn_route_gather(x, undo, offsets, *, out=None, stream=None):
     slots of dropped entries."""
     shp = _route_args(x, "x", False, undo, offsets)
     with _launching(x.device, stream) as st:
-        out = _out(out, "out", x.dtype, (undo.numel(), x.shape[1]), x)
+        out = _out(out, "out", x.dtype, (undo.numel(), x.shape[1]), x, x=x, undo=undo,
+                   offsets=offsets)
         _check(lib().lsh_attn_route_gather(ctypes.byref(shp), _at(x), _at(undo), _at(offsets),
                                            _at(out), st))
     return out
@@ -722,7 +742,8 @@ def lsh_attn_route_gather_backward(dxs, undo, offsets, *, out=None, stream=None)
     summed in float32."""
     shp = _route_args(dxs, "dxs", True, undo, offsets)
     with _launching(dxs.device, stream) as st:
-        out = _out(out, "out", dxs.dtype, (undo.shape[0], dxs.shape[1]), dxs)
+        out = _out(out, "out", dxs.dtype, (undo.shape[0], dxs.shape[1]), dxs, dxs=dxs, undo=undo,
+                   offsets=offsets)
         _check(lib().lsh_attn_route_gather_backward(ctypes.byref(shp), _at(dxs), _at(undo),
                                                     _at(offsets), _at(out), st))
     return out
@@ -734,7 +755,8 @@ def lsh_attn_route_combine(y, weights, undo, offsets, *, out=None, stream=None):
     shp = _route_args(y, "y", True, undo, offsets)
     _cuda(weights, "weights", torch.float32, undo.shape, y)
     with _launching(y.device, stream) as st:
-        out = _out(out, "out", y.dtype, (undo.shape[0], y.shape[1]), y)
+        out = _out(out, "out", y.dtype, (undo.shape[0], y.shape[1]), y, y=y, weights=weights,
+                   undo=undo, offsets=offsets)
         _check(lib().lsh_attn_route_combine(ctypes.byref(shp), _at(y), _at(weights), _at(undo),
                                             _at(offsets), _at(out), st))
     return out

@@ -866,6 +866,26 @@ def test_nothing_is_written_past_the_ends():
         assert whole(bx, n * d) and whole(bt, V * d) and whole(bw, need)
 
 
+def test_outputs_over_inputs_are_refused():
+    tok = torch.tensor([3, 0, 2, 1], device=DEV)
+    buf = torch.zeros(12, 16, device=DEV)
+    table, ids = buf[:4], tok.view(4, 1)
+    _, undo, off = lsh.lsh_attn_route_sort(ids, 4)
+    w = torch.ones(4, 1, device=DEV)
+    for call in (lambda: lsh.lsh_attn_embed(tok, table, out=table),
+                 lambda: lsh.lsh_attn_embed(tok, table, out=buf[1:5]),
+                 lambda: lsh.lsh_attn_embed_backward(tok, table, 4, out=table),
+                 lambda: lsh.lsh_attn_embed_backward(tok, buf[8:], 4, init=table, out=buf[1:5]),
+                 lambda: lsh.lsh_attn_route_gather(table, undo, off, out=table),
+                 lambda: lsh.lsh_attn_route_gather_backward(table, undo, off, out=table),
+                 lambda: lsh.lsh_attn_route_combine(table, w, undo, off, out=table)):
+        with pytest.raises(ValueError, match="out lies over"):
+            call()
+    # a gradient added in place is what init is for
+    lsh.lsh_attn_embed_backward(tok, buf[8:] + 1, 4, init=table, out=table)
+    assert bool((buf[:4] == 1).all()) and not bool(buf[4:].any())
+
+
 def test_binding_checks_its_tensors():
     tok = torch.zeros(4, dtype=torch.int64, device=DEV)
     table = torch.zeros(8, 16, device=DEV)

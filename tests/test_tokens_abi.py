@@ -210,6 +210,18 @@ def test_sizes_beyond_32_bits_do_not_wrap(make, names, wide):
             make(**sizes)
 
 
+def test_an_output_may_not_lie_over_an_input():
+    # (the kernels read their inputs while others of their threads write)
+    buf = torch.zeros(64)
+    a, b, c = buf[:16], buf[16:32], buf[8:24]
+    lsh._apart(a, "out", x=b, init=None, undo=buf[32:])
+    lsh._apart(buf[:0], "out", x=buf)
+    lsh._apart(a, "out", x=buf[3:3])
+    for out, other in ((a, a), (a, c), (c, b), (buf, c), (c, buf)):
+        with pytest.raises(ValueError, match="out lies over dxs"):
+            lsh._apart(out, "out", x=b[:0], dxs=other)
+
+
 def test_binding_index_types():
     with pytest.raises(TypeError, match="int32 or int64"):
         lsh._index_code(torch.zeros(2, dtype=torch.int16), "tokens")
