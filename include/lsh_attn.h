@@ -376,9 +376,15 @@ LSH_ATTN_API lsh_status lsh_attn_embed_backward(const lsh_table* shape, const vo
  * The target's exponential is kept apart from the others' sum, so that a loss
  * far below 1 keeps its digits.
  *   x [n, D] dtype; table [V, D] dtype; targets [n] index type; loss, lse
- *   [n] float32 out.  float32 values are taken apart for the tensor cores: an
- *   infinite one makes the logits that it takes part in NaN (not so with
- *   LSH_FLAG_PORTABLE).
+ *   [n] float32 out.
+ * The rows decide which kernels run, and with them the order of the sums: up to
+ * 32 float32 rows (while they fit in shared memory: 32 of D = 1600, 4 of 12800)
+ * run on CUDA cores, bfloat16 and more rows on the tensor cores, more than 2^24
+ * rows or LSH_FLAG_PORTABLE on the portable CUDA-core kernels.  So a row's last
+ * bits may depend on how many rows stand beside it.
+ * A word ruled out by a logit of -inf has no part in the sum.  But where the
+ * tensor cores take float32 values, those are taken apart first, and an infinite
+ * one makes every logit that it takes part in NaN.
  *   workspace: at least lsh_attn_xent_workspace_size() bytes, 256-byte
  *   aligned (may be NULL when that is 0).                                   */
 LSH_ATTN_API lsh_status lsh_attn_xent_workspace_size(const lsh_table* shape, size_t* bytes);
@@ -394,7 +400,12 @@ LSH_ATTN_API lsh_status lsh_attn_xent(const lsh_table* shape, const void* x, con
  *   dx [n, D] dtype out; dtable [V, D] dtype out.  With bfloat16, g is held in
  *   two bfloat16 values, 16 bits, for the two products; they are summed in
  *   float32 and rounded once.
- *   The work is that of the rows that have a target.
+ *   lse is float32, and so exp(z - lse) is off by about |lse| 2^-23 of itself.
+ *   At the target, where 1 is taken from it, that error is absolute: below a loss
+ *   of about |lse| 2^-23 the target's part of the gradient is rounding, its sign
+ *   included.
+ *   The work is that of the rows that have a target, on the tensor cores; dx of
+ *   up to 128 bfloat16 rows and the CUDA-core kernels work on all rows.
  *   workspace: at least lsh_attn_xent_backward_workspace_size() bytes,
  *   256-byte aligned (may be NULL when that is 0).                          */
 LSH_ATTN_API lsh_status lsh_attn_xent_backward_workspace_size(const lsh_table* shape,

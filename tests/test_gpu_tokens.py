@@ -450,6 +450,61 @@ def test_words_at_minus_infinity_take_no_part():
     R.check("loss", loss, (want, bound))
 
 
+@pytest.mark.parametrize("n,dtype", [(1, F32), (4, F32), (7, F32), (16, F32), (32, F32),
+                                     (1, BF16), (20, BF16), (128, BF16), (129, BF16), (300, BF16)])
+def test_words_at_minus_infinity_take_no_part_on_every_path(n, dtype):
+    g = gen(14 + n)
+    x, table = randn(g, n, 72, dtype=dtype).abs(), randn(g, 700, 72, dtype=dtype, scale=0.1)
+    table[10:90, 3] = -float("inf")     # 64 words side by side among them
+    table[650, 71] = -float("inf")
+    keep = torch.cat([torch.arange(10), torch.arange(90, 650), torch.arange(651, 700)]).to(DEV)
+    at = torch.randint(0, keep.numel(), (n,), device=DEV, generator=g)
+    loss, lse = lsh.lsh_attn_xent(x, table, keep[at])
+    want_loss, want_lse = R.xent(x, table[keep], at, 1.0)
+    R.check("lse", lse, want_lse)
+    R.check("loss", loss, want_loss)
+    dloss = randn(g, n)
+    dx, dw = lsh.lsh_attn_xent_backward(x, table, keep[at], lse, dloss)
+    _, want_dw = R.xent_backward(x, table[keep], at, dloss, 1.0, BF16 if dtype == BF16 else None)
+    R.check("dtable", dw[keep], want_dw)
+    assert not bool(dw[10:90].any()) and not bool(dw[650].any())
+    # (0 times -inf: these columns alone have no value)
+    assert bool(torch.isnan(dx[:, 3]).all()) and bool(torch.isfinite(dx[:, 4:71].float()).all())
+
+
+def test_infinite_float32_words_on_the_tensor_cores_are_nan():
+    x, table, t, _ = make_xent(33, 300, 72, F32, torch.int64, 0)
+    table[11, 3] = -float("inf")
+    loss, lse = lsh.lsh_attn_xent(x, table, t)
+    assert bool(torch.isnan(lse).all()) and bool(torch.isnan(loss).all())
+
+
+@pytest.mark.parametrize("n,dtype", [(20, F32), (40, F32), (20, BF16), (300, BF16)])
+@pytest.mark.parametrize("portable", [False, True])
+def test_gradient_of_sure_rows_is_off_by_the_rounding_of_lse(n, dtype, portable):
+    # dx for a table of unit vectors is g itself.  z stands near 20 and the
+    # losses lie between exp(-4) and exp(-30); lse rounds by 2^-24 of itself,
+    # log2's units of both by as much again, 16 products by 22 steps of 2^-23
+    # as above; g's own 2^-16 on top.
+    d = 16
+    g = gen(n)
+    t = torch.randint(0, d, (n,), device=DEV, generator=g)
+    table = torch.eye(d, device=DEV, dtype=dtype)
+    x = torch.zeros(n, d, device=DEV)
+    x[torch.arange(n, device=DEV), t] = 4 + 26 * torch.rand(n, device=DEV, generator=g)
+    x = x.to(dtype)
+    lse = lsh.lsh_attn_xent(x, table, t, portable=portable)[1]
+    dx, _ = lsh.lsh_attn_xent_backward(x, table, t, lse, torch.ones(n, device=DEV),
+                                       portable=portable)
+    z = x.double()
+    p = torch.softmax(z, 1)
+    others = torch.where(torch.nn.functional.one_hot(t, d).bool(), torch.zeros_like(p), p)
+    want = others - torch.nn.functional.one_hot(t, d) * others.sum(1, keepdim=True)
+    err = p * (26 * 2.0 ** -23 * z.amax(1, keepdim=True) + 2.0 ** -21)
+    size = want.abs() + err
+    R.check("dx", dx, (want, err + size * (R.half_step(dtype) + 2.0 ** -15)))
+
+
 @pytest.mark.parametrize("portable", [False, True])
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_words_masked_by_the_lowest_value_take_no_part(dtype, portable):
