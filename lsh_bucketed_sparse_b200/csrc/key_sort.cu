@@ -34,6 +34,10 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kPer = 8;                       // entries per thread
 constexpr int kTile = kThreads * kPer;
 constexpr int kScanThreads = 1024;
+// Tiles whose counts every CTA of the scatter adds up for itself; above it one
+// CTA does so for all, in a launch of its own.  Order by 8 / 256 / 1023 experts, us,
+// for itself and in its own launch: 64 tiles 14 / 18 / 25 and 16 / 21 / 23, 128 tiles
+// 18 / 20 / 31 and 18 / 23 / 29, 512 tiles 41 / 78 / 158 and 33 / 49 / 72.
 constexpr int kFusedTiles = 64;
 constexpr int kOneDigitBits = 10;
 constexpr int kMaxBins = 1 << 11;
