@@ -400,9 +400,9 @@ LSH_ATTN_API lsh_status lsh_attn_xent(const lsh_table* shape, const void* x, con
  *   dx [n, D] dtype out; dtable [V, D] dtype out.  With bfloat16, g is held in
  *   two bfloat16 values, 16 bits, for the two products; they are summed in
  *   float32 and rounded once.
- *   lse is float32, and so exp(z - lse) is off by about |lse| 2^-23 of itself.
+ *   lse is float32, and so exp(z - lse) is off by about |lse| 2^-24 of itself.
  *   At the target, where 1 is taken from it, that error is absolute: below a loss
- *   of about |lse| 2^-23 the target's part of the gradient is rounding, its sign
+ *   of about |lse| 2^-24 the target's part of the gradient is rounding, its sign
  *   included.
  *   The work is that of the rows that have a target, on the tensor cores; dx of
  *   up to 128 bfloat16 rows and the CUDA-core kernels work on all rows.

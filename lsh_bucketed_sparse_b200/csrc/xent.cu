@@ -15,14 +15,16 @@ constexpr int kThreads = 256;
 // lse_i = log(R_i + exp z_i,t_i), loss_i = lse_i - z_i,t_i = log1p(R_i / exp
 // z_i,t_i), where R_i = s 2^m is the slices' sum, which leaves the target out: the
 // loss of a row that is sure of its target keeps its digits, where 1 + R_i and
-// the difference of two logits would cut them off.  A block joins 32 rows: each
-// warp every kJoinWarps-th slice, then the warps in order.
+// the difference of two logits would cut them off.  lse is what the gradient
+// takes its probabilities from: for such a row z_i,t_i + loss_i in one rounding.
+// A block joins 32 rows: each warp every kJoinWarps-th slice, then the warps in
+// order.
 constexpr int kJoinWarps = kThreads / 32;
 template <typename I>
 __global__ void __launch_bounds__(kThreads)
 xent_join_kernel(const float2* __restrict__ part, const float* __restrict__ zt,
                  const I* __restrict__ targets, float* __restrict__ loss, float* __restrict__ lse,
-                 int rows, int slices, int vocab, float unit) {
+                 int rows, int slices, int vocab, float scale) {
   __shared__ float2 sums[kJoinWarps][32];
   wait_prior_grid();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -45,6 +47,7 @@ xent_join_kernel(const float2* __restrict__ part, const float* __restrict__ zt,
     loss[row] = 0.f;
     return;
   }
+  const float unit = scale * kLog2e;
   const float z = zt[row], d = fmaf(-z, unit, m);  // m against the target, in one rounding
   if (unit == 0.f) {  // all logits are 0, the target's among s
     lse[row] = loss[row] = (d + log2f(s)) * kLn2;
@@ -53,7 +56,7 @@ xent_join_kernel(const float2* __restrict__ part, const float* __restrict__ zt,
   const float over = d > 0.f ? (d + log2f(s + exp2f(-d))) * kLn2 : log1pf(s * exp2f(d));
   lse_add(m, s, z * unit, 1.f);
   const float all = (m + log2f(s)) * kLn2;
-  lse[row] = all;
+  lse[row] = over <= 1.f && !isnan(all) ? fmaf(z, scale, over) : all;
   loss[row] = isnan(all) ? all : over;
 }
 
@@ -133,16 +136,14 @@ cudaError_t launch_xent(const TableProblem& p, const void* x, const void* table,
                       : launch_xent_portable(p, x, table, targets, part, zt, st);
   if (e) return e;
   const dim3 grid((rows + 31) / 32), block(kThreads);
-  const float unit =
-      !xent_few_supported(p) && xent_tc_supported(p) ? p.scale * kLog2e : 1.f;  // of zt
   e = p.idx64 ? launch_dependent(xent_join_kernel<int64_t>, grid, block, 0, st,
                                  static_cast<const float2*>(part), static_cast<const float*>(zt),
                                  static_cast<const int64_t*>(targets), loss, lse, rows, slices,
-                                 p.vocab, unit)
+                                 p.vocab, p.scale)
               : launch_dependent(xent_join_kernel<int32_t>, grid, block, 0, st,
                                  static_cast<const float2*>(part), static_cast<const float*>(zt),
                                  static_cast<const int32_t*>(targets), loss, lse, rows, slices,
-                                 p.vocab, unit);
+                                 p.vocab, p.scale);
   if (e == cudaSuccess) note_launch();
   return e;
 }

@@ -32,9 +32,8 @@ cudaError_t launch_xent_clean(const TableProblem& p, const void* x, const void* 
                               void* clean, cudaStream_t st);
 
 // Forward, of any kind: part[slice][row] = (maximum, sum) over the slice's logits
-// except the target's, which stands in zt[row] where the row has a target: in
-// log2, or from the tensor cores as the product left it, without scale (where
-// scale is 0 the sum has it too).
+// except the target's, which stands in zt[row] where the row has a target, as the
+// product left it, without scale (where scale is 0 the sum has it too).
 
 // Most bytes of g in a piece of the backward: `most`, or less by the test hook.
 size_t xent_piece_bytes(size_t most);

@@ -63,11 +63,7 @@ __global__ void __launch_bounds__(logit_threads(kRows), 1) xent_few_logits_kerne
   const int row = lane * kMine / R, r0 = lane * kMine % R;
   const int target = row < p.n ? target_of(targets, row, p.vocab) : -1;
   const float c = p.scale * kLog2e;
-  float run_m = -INFINITY, run_s = 0.f, up = 0.f, lse2 = 0.f;
-  if (kGrad && target >= 0) {
-    up = p.dloss[row] * p.scale;
-    lse2 = p.lse[row] * kLog2e;
-  }
+  float run_m = -INFINITY, run_s = 0.f;
   const int stride = gridDim.x * kLogitWarps * R;
   for (int w0 = (blockIdx.x * kLogitWarps + warp) * R; w0 < p.vocab; w0 += stride) {
     float a[kSums];
@@ -122,12 +118,15 @@ __global__ void __launch_bounds__(logit_threads(kRows), 1) xent_few_logits_kerne
         continue;
       }
       if (kGrad) {
-        const float e = exp2f(fmaf(a[t], c, -lse2)) - (word == target ? 1.f : 0.f);
-        p.g[(size_t)word * kRows + row] = target >= 0 ? up * e : 0.f;
+        float g = 0.f;
+        if (target >= 0) {  // (read here: the sums leave no registers for them)
+          const float e = exp2f(fmaf(a[t], p.scale, -p.lse[row]) * kLog2e);
+          g = p.dloss[row] * p.scale * (e - (word == target ? 1.f : 0.f));
+        }
+        p.g[(size_t)word * kRows + row] = g;
       } else {
-        const float z = a[t] * c;
-        if (word == target) p.zt[row] = z;
-        else lse_add(run_m, run_s, z, 1.f);
+        if (word == target) p.zt[row] = a[t];
+        if (word != target || c == 0.f) lse_add(run_m, run_s, a[t] * c, 1.f);
       }
     }
   }

@@ -98,9 +98,8 @@ xent_fwd_kernel(const Operand<T> x, const Operand<T> w, const I* __restrict__ ta
       for (int j = 0; j < 4; ++j) {
         const int v = n0 + 4 * tx + j;
         if (v >= v1) continue;
-        const float z = acc[i][j] * scale2;
-        if (v == t[i]) zt[m0 + 4 * ty + i] = z;
-        else lse_add(m[i], sum[i], z, 1.f);
+        if (v == t[i]) zt[m0 + 4 * ty + i] = acc[i][j];
+        if (v != t[i] || scale2 == 0.f) lse_add(m[i], sum[i], acc[i][j] * scale2, 1.f);
       }
   }
 #pragma unroll

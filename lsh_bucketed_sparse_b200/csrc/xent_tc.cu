@@ -430,14 +430,14 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
       const Item it = decode(g, item);
       const int row0 = it.m * kTileM + rank * 128 + quad * 32, row = row0 + lane;
       int target = -1;
-      float run_m = -INFINITY, run_s = 0.f, up = 0.f, lse2 = 0.f;
+      float run_m = -INFINITY, run_s = 0.f, up = 0.f, lse = 0.f;
       if constexpr (kEpi == Epi::kLse || kEpi == Epi::kGrad) {
         if (row < g.rows) {
           if constexpr (kEpi == Epi::kGrad) {
             const int at = p.order[row];
             target = target_of(targets, at, p.vocab);
             up = p.dloss[at] * p.scale;
-            lse2 = p.lse[at] * kLog2e;
+            lse = p.lse[at];
           } else {
             target = target_of(targets, row, p.vocab);
           }
@@ -482,10 +482,13 @@ xent_tc_kernel(const __grid_constant__ CUtensorMap amap, const __grid_constant__
             run_m = top;
           }
         } else if constexpr (kEpi == Epi::kGrad) {
-          const float2 c2 = make_float2(c, c), l2 = make_float2(-lse2, -lse2);
+          // (the difference before the units of log2: what rounding is left of a
+          // sure row's target, next to 1, is that of lse)
+          const float2 s2 = make_float2(p.scale, p.scale), l2 = make_float2(-lse, -lse);
+          const float2 log2e = make_float2(kLog2e, kLog2e);
 #pragma unroll
           for (int i = 0; i < 32; i += 2) {
-            const float2 e = fma2(make_float2(z[i], z[i + 1]), c2, l2);
+            const float2 e = mul2(fma2(make_float2(z[i], z[i + 1]), s2, l2), log2e);
             z[i] = ex2(e.x);
             z[i + 1] = ex2(e.y);
           }

@@ -506,6 +506,37 @@ def test_gradient_of_sure_rows_is_off_by_the_rounding_of_lse(n, dtype, portable)
 
 
 @pytest.mark.parametrize("portable", [False, True])
+@pytest.mark.parametrize("scale", [1.0, -0.37])
+@pytest.mark.parametrize("n", [2, 30, 60, 400])
+def test_gradient_of_sure_rows_is_off_by_half_a_step_of_lse(n, scale, portable):
+    # as above, with logits of one exact product each.  lse = z scale + loss in
+    # one rounding, half a step of it; the loss itself 64 half steps of its own;
+    # z scale - lse in one rounding and log2's unit in another, 2^-24 each of the
+    # difference; the exponential 2 steps of 2^-22.
+    d = 16
+    g = gen(n + 1)
+    t = torch.randint(0, d, (n,), device=DEV, generator=g)
+    table = torch.eye(d, device=DEV)
+    x = torch.zeros(n, d, device=DEV)
+    x[torch.arange(n, device=DEV), t] = (4 + 36 * torch.rand(n, device=DEV, generator=g)) / scale
+    lse = lsh.lsh_attn_xent(x, table, t, scale=scale, portable=portable)[1]
+    up = randn(g, n)
+    dx, _ = lsh.lsh_attn_xent_backward(x, table, t, lse, up, scale=scale, portable=portable)
+    z = x.double() * float(torch.tensor(scale))
+    p, full = torch.softmax(z, 1), torch.logsumexp(z, 1, keepdim=True)
+    hot = torch.nn.functional.one_hot(t, d).bool()
+    others = torch.where(hot, torch.zeros_like(p), p)
+    loss = others.sum(1, keepdim=True) / p.gather(1, t[:, None])
+    R.check("lse", lse, (full[:, 0], (2.0 ** -24 * full + 2.0 ** -18 * loss)[:, 0]))
+    want = torch.where(hot, -others.sum(1, keepdim=True), others)
+    err = p * (2.0 ** -24 * full + 2.0 ** -18 * loss + 2.0 ** -23 * (z - full).abs() + 2.0 ** -21)
+    up = (up.double() * float(torch.tensor(scale)))[:, None]
+    size = up.abs() * (want.abs() + err)
+    # (planes of g, the roundings of up and of the products with it)
+    R.check("dx", dx, (up * want, up.abs() * err + size * 2.0 ** -20 + 1e-35))
+
+
+@pytest.mark.parametrize("portable", [False, True])
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_words_masked_by_the_lowest_value_take_no_part(dtype, portable):
     # x's last column is 1, a masked word's entry there the type's lowest value
