@@ -512,13 +512,19 @@ def make_route_shape(tokens, top_k, n_experts, d_model=8, dtype=torch.bfloat16,
 class _launching:
     """Makes ``device`` and ``stream`` current (the device's own current stream
     when None), so that what is allocated inside belongs to the stream the
-    kernels run on, and gives the stream's handle.  Costs nothing more where
-    the device is the current one already."""
+    kernels run on, and gives the stream's handle.  The caller's ``tensors`` are
+    recorded on a stream that is handed over, so that their memory is not given
+    away under its kernels when the caller lets go of them.  Costs nothing more
+    where the device is the current one already."""
     __slots__ = ("device", "stream", "held")
 
-    def __init__(self, device, stream):
-        if stream is not None and stream.device != device:
-            raise ValueError(f"stream is on {stream.device}, expected {device}")
+    def __init__(self, device, stream, *tensors):
+        if stream is not None:
+            if stream.device != device:
+                raise ValueError(f"stream is on {stream.device}, expected {device}")
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(stream)
         self.device, self.stream, self.held = device, stream, ()
 
     def __enter__(self):
@@ -591,7 +597,7 @@ def lsh_attn_embed(tokens, table, *, scale=1.0, out=None, stream=None):
     _cuda(tokens, "tokens")
     V, D = _table(table, None, tokens)
     shp = make_table_shape(tokens.numel(), V, D, table.dtype, _index_code(tokens, "tokens"), scale)
-    with _launching(tokens.device, stream) as st:
+    with _launching(tokens.device, stream, tokens, table, out) as st:
         out = _out(out, "out", table.dtype, (*tokens.shape, D), tokens, tokens=tokens,
                    table=table)
         _check(lib().lsh_attn_embed(ctypes.byref(shp), _at(tokens), _at(table), _at(out), st))
@@ -618,7 +624,7 @@ def lsh_attn_embed_backward(tokens, dout, vocab, *, scale=1.0, init=None, out=No
         _cuda(init, "init", dout.dtype, (vocab, D), tokens)
     shp = make_table_shape(tokens.numel(), vocab, D, dout.dtype, _index_code(tokens, "tokens"),
                            scale)
-    with _launching(tokens.device, stream) as st:
+    with _launching(tokens.device, stream, tokens, dout, init, out, workspace) as st:
         need = lsh_attn_embed_backward_workspace_size(shp)
         # (init may be out itself: each row is read before it is written)
         over = out is not None and init is not None and init.data_ptr() == out.data_ptr()
@@ -652,7 +658,7 @@ def lsh_attn_xent(x, table, targets, *, scale=1.0, workspace=None, portable=Fals
     [V, D], the logits scale * x @ table.T never stored.  Returns (loss, lse),
     float32 [...]; loss is 0 where the target is outside the table."""
     shp = _xent_args(x, table, targets, scale, portable)
-    with _launching(x.device, stream) as st:
+    with _launching(x.device, stream, x, table, targets, workspace) as st:
         need = lsh_attn_xent_workspace_size(shp)
         loss = x.new_empty(targets.shape, dtype=torch.float32)
         lse = torch.empty_like(loss)
@@ -673,7 +679,7 @@ def lsh_attn_xent_backward(x, table, targets, lse, dloss, *, scale=1.0, workspac
     shp = _xent_args(x, table, targets, scale, portable)
     _cuda(lse, "lse", torch.float32, targets.shape, x)
     _cuda(dloss, "dloss", torch.float32, targets.shape, x)
-    with _launching(x.device, stream) as st:
+    with _launching(x.device, stream, x, table, targets, lse, dloss, workspace) as st:
         need = lsh_attn_xent_backward_workspace_size(shp)
         dx, dtable = torch.empty_like(x), torch.empty_like(table)
         ws, n = _workspace(workspace, need, x)
@@ -698,7 +704,7 @@ def lsh_attn_route_sort(experts, n_experts, *, workspace=None, stream=None):
         raise ValueError(f"experts must be [tokens, top_k], got shape {tuple(experts.shape)}")
     T, k = experts.shape
     shp = make_route_shape(T, k, n_experts, index_type=_index_code(experts, "experts"))
-    with _launching(experts.device, stream) as st:
+    with _launching(experts.device, stream, experts, workspace) as st:
         need = lsh_attn_route_sort_workspace_size(shp)
         perm = experts.new_empty(T * k, dtype=torch.int32)
         undo = experts.new_empty((T, k), dtype=torch.int32)
@@ -729,7 +735,7 @@ def lsh_attn_route_gather(x, undo, offsets, *, out=None, stream=None):
     """Tokens in their experts' order: x [T, D] to [T * k, D], zero rows in the
     slots of dropped entries."""
     shp = _route_args(x, "x", False, undo, offsets)
-    with _launching(x.device, stream) as st:
+    with _launching(x.device, stream, x, undo, offsets, out) as st:
         out = _out(out, "out", x.dtype, (undo.numel(), x.shape[1]), x, x=x, undo=undo,
                    offsets=offsets)
         _check(lib().lsh_attn_route_gather(ctypes.byref(shp), _at(x), _at(undo), _at(offsets),
@@ -741,7 +747,7 @@ def lsh_attn_route_gather_backward(dxs, undo, offsets, *, out=None, stream=None)
     """The gather's gradient: [T, D], each token's kept rows of dxs [T * k, D]
     summed in float32."""
     shp = _route_args(dxs, "dxs", True, undo, offsets)
-    with _launching(dxs.device, stream) as st:
+    with _launching(dxs.device, stream, dxs, undo, offsets, out) as st:
         out = _out(out, "out", dxs.dtype, (undo.shape[0], dxs.shape[1]), dxs, dxs=dxs, undo=undo,
                    offsets=offsets)
         _check(lib().lsh_attn_route_gather_backward(ctypes.byref(shp), _at(dxs), _at(undo),
@@ -754,7 +760,7 @@ def lsh_attn_route_combine(y, weights, undo, offsets, *, out=None, stream=None):
     kept rows times weights [T, k] (float32), summed in float32."""
     shp = _route_args(y, "y", True, undo, offsets)
     _cuda(weights, "weights", torch.float32, undo.shape, y)
-    with _launching(y.device, stream) as st:
+    with _launching(y.device, stream, y, weights, undo, offsets, out) as st:
         out = _out(out, "out", y.dtype, (undo.shape[0], y.shape[1]), y, y=y, weights=weights,
                    undo=undo, offsets=offsets)
         _check(lib().lsh_attn_route_combine(ctypes.byref(shp), _at(y), _at(weights), _at(undo),
@@ -768,7 +774,7 @@ def lsh_attn_route_combine_backward(dout, y, weights, undo, offsets, *, stream=N
     shp = _route_args(y, "y", True, undo, offsets)
     _cuda(weights, "weights", torch.float32, undo.shape, y)
     _cuda(dout, "dout", y.dtype, (undo.shape[0], y.shape[1]), y)
-    with _launching(y.device, stream) as st:
+    with _launching(y.device, stream, dout, y, weights, undo, offsets) as st:
         dy = torch.empty_like(y)
         dw = torch.empty_like(weights)
         _check(lib().lsh_attn_route_combine_backward(ctypes.byref(shp), _at(dout), _at(y),

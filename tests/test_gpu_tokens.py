@@ -894,6 +894,50 @@ def test_calls_on_another_stream():
     assert torch.equal(loss, lsh.lsh_attn_xent(out, table, targets)[0])
 
 
+def test_memory_let_go_is_kept_for_the_stream_handed_over():
+    # the caller's tensors die while the stream has not begun to read them; what
+    # is allocated next on the caller's own stream may not take their memory
+    g = gen(41)
+    T, V, D, k = 1001, 500, 64, 2
+    table, x0 = randn(g, V, D), randn(g, T, D)
+    tok, ids = make_tokens(g, T, V, torch.int64), make_tokens(g, T * k, 9, torch.int32).view(T, k)
+    lse, up = torch.rand(T, device=DEV, generator=g) + 5, randn(g, T)
+    _, undo, off = lsh.lsh_attn_route_sort(ids, 9)
+    y, w = randn(g, T * k, D), torch.rand(T, k, device=DEV, generator=g)
+    calls = {
+        "embed": (lsh.lsh_attn_embed, (tok, table), {}),
+        "embed_backward": (lsh.lsh_attn_embed_backward, (tok, x0, V), dict(init=table)),
+        "xent": (lsh.lsh_attn_xent, (x0, table, tok), {}),
+        "xent_backward": (lsh.lsh_attn_xent_backward, (x0, table, tok, lse, up), {}),
+        "sort": (lsh.lsh_attn_route_sort, (ids, 9), {}),
+        "gather": (lsh.lsh_attn_route_gather, (x0, undo, off), {}),
+        "gather_backward": (lsh.lsh_attn_route_gather_backward, (y, undo, off), {}),
+        "combine": (lsh.lsh_attn_route_combine, (y, w, undo, off), {}),
+        "combine_backward": (lsh.lsh_attn_route_combine_backward, (x0, y, w, undo, off), {}),
+    }
+
+    def tensors(out):
+        return out if isinstance(out, tuple) else (out,)
+
+    s = torch.cuda.Stream()
+    for name, (call, args, kw) in calls.items():
+        want = tensors(call(*args, **kw))
+        own = [a.clone() if isinstance(a, torch.Tensor) else a for a in args]
+        own_kw = {n: a.clone() for n, a in kw.items()}
+        sizes = [a.numel() * a.element_size() for a in (*own, *own_kw.values())
+                 if isinstance(a, torch.Tensor)]
+        torch.cuda.synchronize()
+        with torch.cuda.stream(s):
+            torch.cuda._sleep(20_000_000)        # some 10 ms
+        got = tensors(call(*own, **own_kw, stream=s))
+        del own, own_kw
+        taken = [torch.full((n,), 0x7f, dtype=torch.uint8, device=DEV) for n in sizes]
+        torch.cuda.current_stream().wait_stream(s)
+        for a, b in zip(got, want):
+            assert torch.equal(a, b), name
+        del taken
+
+
 def test_two_streams_at_once():
     a, b = _step_inputs(5, BF16, n=3001), _step_inputs(6, BF16, n=2500)
     want_a, want_b = _step(*a), _step(*b)
